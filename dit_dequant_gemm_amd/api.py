@@ -35,6 +35,20 @@ class GemmDesc(ctypes.Structure):
                 ("m", _c_i64), ("k", _c_i64), ("n", _c_i64), ("bits", _c_int), ("y_dtype", _c_int)]
 
 
+class RopeTensor(ctypes.Structure):
+    """ddg_rope_tensor: heads to rotate, with their strides in elements."""
+    _fields_ = [("x", _vp), ("y", _vp), ("weight", _vp), ("heads", _c_i64),
+                ("x_batch", _c_i64), ("x_token", _c_i64), ("x_head", _c_i64),
+                ("y_batch", _c_i64), ("y_token", _c_i64), ("y_head", _c_i64)]
+
+
+class RopeDesc(ctypes.Structure):
+    """ddg_rope_desc: positions, frequencies and layout of a rotation."""
+    _fields_ = [("positions", _vp), ("positions_batch", _c_i64), ("freqs", _vp), ("axes", _c_int),
+                ("sections", _c_int * 4), ("rot_dim", _c_int), ("layout", _c_int), ("inverse", _c_int),
+                ("amplitude", ctypes.c_float)]
+
+
 MAX_GROUPED = 256
 SIGNATURES = {
     "ddg_version": (_c_int, []),
@@ -56,6 +70,12 @@ SIGNATURES = {
     "ddg_lowrank_fused_gemm_noalloc": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _c_int, _c_i64, _vp, _vp,
                                                 _c_int, _vp, _c_int, _vp]),
     "ddg_rpbh_rotate": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _vp, _c_int, _vp, _c_int, _vp]),
+    "ddg_rope": (_c_int, [ctypes.POINTER(RopeTensor), _c_int, _c_i64, _c_i64, _c_int, ctypes.POINTER(RopeDesc), _vp]),
+    "ddg_qk_norm_rope": (_c_int, [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), _c_int, _c_int, _c_i64,
+                                  _c_i64, _c_int, _c_int, ctypes.c_float, ctypes.POINTER(RopeDesc), _vp]),
+    "ddg_rope_frequencies": (_c_int, [_c_int, ctypes.c_double, _c_int, ctypes.c_double, ctypes.c_double,
+                                      ctypes.c_double, ctypes.c_double, ctypes.POINTER(ctypes.c_double),
+                                      ctypes.POINTER(ctypes.c_double)]),
     "ddg_fp4_quantize_pack": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_int, _vp, _vp, _vp]),
     "ddg_fp8_quantize_rows": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _vp]),
     "ddg_w4a8_gemm": (_c_int, [_vp, _vp, _c_i64, _c_i64, _vp, _vp, _c_int, _c_i64, _vp, _c_int, _vp]),
@@ -124,6 +144,25 @@ def _stream_ptr(device: torch.device) -> int:
         idx = device.index
         return _RAW_STREAM(torch.cuda.current_device() if idx is None else idx)
     return torch.cuda.current_stream(device).cuda_stream
+
+
+class _NoSwitch:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NO_SWITCH = _NoSwitch()
+
+
+def _device_of(t: torch.Tensor):
+    """Context in which t's device is the current one (the library launches on
+    the current device); nothing to do, and nothing spent, when it already is."""
+    if not t.is_cuda or t.device.index in (None, torch.cuda.current_device()):
+        return _NO_SWITCH
+    return torch.cuda.device(t.device)
 
 
 def _require_cuda(t: torch.Tensor, name: str) -> None:
@@ -241,6 +280,167 @@ def rpbh_rotate(x: torch.Tensor, perm: torch.Tensor, signs: torch.Tensor, h: int
                                           signs.data_ptr(), h, out.data_ptr(), code[odt],
                                           _stream_ptr(x.device)), "ddg_rpbh_rotate")
     return out
+
+
+# ------------------------------------------------------------------ rotary positions
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_NORMS = {"head": 1, "token": 2}
+ROPE_MAX_AXES, ROPE_MAX_HEAD_DIM = 4, 512
+
+
+def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device="cuda"):
+    """(freqs, amplitude) of `dim` rotated values for rope and qk_norm_rope:
+    dim / 2 float64 radians per position, base^(-2i/dim), scaled for contexts
+    `factor` times longer: "linear" (positions interpolated), "ntk" (a larger
+    base) or "yarn" (pairs that turn often over original_length keep their
+    frequency; amplitude 0.1 ln(factor) + 1).  With several position axes,
+    concatenate the frequencies of each axis and pass the pair counts as
+    `sections`."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    if not 2 <= dim <= ROPE_MAX_HEAD_DIM or dim % 2:
+        raise ValueError(f"dim must be even and within 2..{ROPE_MAX_HEAD_DIM}")
+    out = (ctypes.c_double * (dim // 2))()
+    amplitude = ctypes.c_double()
+    _check(load_library().ddg_rope_frequencies(dim, base, ROPE_SCALINGS[scaling], factor, original_length, beta_fast,
+                                               beta_slow, out, ctypes.byref(amplitude)), "ddg_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64, device=device), amplitude.value
+
+
+def _heads_view(t: torch.Tensor, name: str, like=None):
+    """(tensor as batch x tokens x heads x dim, strides) of a 3-D or 4-D GPU
+    tensor whose last dimension is dense."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be bf16 or float32")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be ([batch,] tokens, heads, head_dim)")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} has the wrong shape, dtype or device")
+    st = t.stride()
+    return (st[0], st[1], st[2]) if t.dim() == 4 else (0, st[0], st[1])
+
+
+def _rope_tensor(x: torch.Tensor, out: Optional[torch.Tensor], weight: Optional[torch.Tensor], name: str):
+    xs = _heads_view(x, name)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    ys = _heads_view(out, f"out of {name}", x)
+    return RopeTensor(x.data_ptr(), out.data_ptr(), None if weight is None else weight.data_ptr(), x.shape[-2],
+                      *xs, *ys), out
+
+
+def _rope_desc(x: torch.Tensor, positions, freqs, layout: str, sections, amplitude: float, inverse: bool):
+    """(RopeDesc, tensors it points into) for heads x, its positions checked
+    against x's batch and tokens."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+    d = RopeDesc(axes=1, layout=ROPE_LAYOUTS[layout], inverse=int(bool(inverse)), amplitude=amplitude)
+    if freqs is None:
+        if positions is not None or sections is not None:
+            raise ValueError("positions and sections need freqs")
+        return d
+    if positions is None:
+        raise ValueError("freqs need positions")
+    for t, name in ((positions, "positions"), (freqs, "freqs")):
+        _require_cuda(t, name)
+        if t.device != x.device:
+            raise ValueError(f"{name} must be on the device of the heads")
+    if freqs.dtype != torch.float64 or freqs.dim() != 1:
+        raise ValueError("freqs must be a 1-D float64 tensor")
+    if positions.dtype != torch.int32:
+        raise ValueError("positions must be int32")
+    pairs = freqs.shape[0]
+    sections = (pairs,) if sections is None else tuple(int(s) for s in sections)
+    if not 1 <= len(sections) <= ROPE_MAX_AXES or min(sections) < 0 or sum(sections) != pairs:
+        raise ValueError(f"sections must be 1 to {ROPE_MAX_AXES} pair counts that add up to len(freqs)")
+    batch, tokens = (x.shape[0], x.shape[1]) if x.dim() == 4 else (1, x.shape[0])
+    axes = len(sections)
+    shape = tuple(positions.shape)
+    if axes == 1 and shape in ((tokens,), (tokens, 1)):
+        per_batch = False
+    elif axes > 1 and shape == (tokens, axes):
+        per_batch = False
+    elif x.dim() == 4 and (shape == (batch, tokens, axes) or (axes == 1 and shape == (batch, tokens))):
+        per_batch = True
+    else:
+        raise ValueError("positions must be (tokens, axes) or (batch, tokens, axes)")
+    d.positions, d.freqs = positions.data_ptr(), freqs.data_ptr()
+    d.positions_batch = tokens * axes if per_batch else 0
+    d.axes, d.rot_dim = axes, 2 * pairs
+    for i, s in enumerate(sections):
+        d.sections[i] = s
+    return d
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout: str = "interleaved",
+         sections=None, amplitude: float = 1.0, inverse: bool = False,
+         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Heads x ([batch,] tokens, heads, head_dim; bf16 or float32, the last
+    dimension dense, other strides free) with the first 2 len(freqs) values of
+    every head turned by their token's position times freqs (float64; see
+    rope_frequencies).  positions: int32 (tokens,) or (tokens, axes), or the
+    same with a leading batch; sections: pairs of each axis.  inverse turns
+    back (the gradient of the rotation).  out may be x itself."""
+    with _device_of(x):
+        t, out = _rope_tensor(x, out, None, "x")
+        if freqs is None:
+            raise ValueError("rope needs positions and freqs")
+        d = _rope_desc(x, positions, freqs, layout, sections, amplitude, inverse)
+        batch, tokens = (x.shape[0], x.shape[1]) if x.dim() == 4 else (1, x.shape[0])
+        _check(load_library().ddg_rope(ctypes.byref(t), DDG_F32 if x.dtype == torch.float32 else DDG_BF16, batch,
+                                       tokens, x.shape[-1], ctypes.byref(d), _stream_ptr(x.device)), "ddg_rope")
+    return out
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 freqs: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, norm: str = "head",
+                 layout: str = "interleaved", sections=None, amplitude: float = 1.0,
+                 out_q: Optional[torch.Tensor] = None, out_k: Optional[torch.Tensor] = None):
+    """(q, k) after a root-mean-square norm of every head (norm="head",
+    weights of head_dim values) or over all heads of a token ("token", weights
+    of heads * head_dim) and the rotation of rope, in one pass with one
+    rounding.  q and k may have different head counts (k may be None); both
+    may be slices of the fused projection's output, and each may be its own
+    output.  freqs None: the norms alone."""
+    if norm not in ROPE_NORMS:
+        raise ValueError(f"norm must be one of {sorted(ROPE_NORMS)}")
+    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]
+                          or k.dtype != q.dtype or k.device != q.device):
+        raise ValueError("q and k must agree but for their head counts")
+    if k is None and (k_weight is not None or out_k is not None):
+        raise ValueError("k_weight and out_k need k")
+    wdt = None
+    for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
+        if w is None:
+            continue
+        _require_cuda(w, name)
+        size = t.shape[-1] * (t.shape[-2] if norm == "token" else 1)
+        if w.dtype not in (torch.bfloat16, torch.float32) or w.numel() != size or w.device != q.device:
+            raise ValueError(f"{name} must hold {size} bf16 or float32 values on the device of q")
+        if wdt not in (None, w.dtype):
+            raise ValueError("q_weight and k_weight must have one dtype")
+        wdt = w.dtype
+    with _device_of(q):
+        tq, out_q = _rope_tensor(q, out_q, q_weight, "q")
+        tk = None
+        if k is not None:
+            tk, out_k = _rope_tensor(k, out_k, k_weight, "k")
+        d = _rope_desc(q, positions, freqs, layout, sections, amplitude, False)
+        batch, tokens = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
+        _check(load_library().ddg_qk_norm_rope(
+            ctypes.byref(tq), None if tk is None else ctypes.byref(tk),
+            DDG_F32 if q.dtype == torch.float32 else DDG_BF16, DDG_F32 if wdt == torch.float32 else DDG_BF16,
+            batch, tokens, q.shape[-1], ROPE_NORMS[norm], eps, ctypes.byref(d), _stream_ptr(q.device)),
+            "ddg_qk_norm_rope")
+    return out_q, out_k
 
 
 class QWeightFP4:

@@ -2,6 +2,7 @@
 // host, kernel choice, launch.  No allocation, no synchronization.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <random>
@@ -689,6 +690,191 @@ int ddg_rpbh_rotate(const void* x, int x_dtype, int64_t n, int64_t d, const int3
   if (int st = device_info(&cus)) return st;
   return hip_status(ddg::launch_rpbh_rotate(x, x_dtype == DDG_F32, n, (int)d, perm, signs, h, out,
                                             out_dtype == DDG_F32, cus, stream));
+}
+
+namespace {
+// The three outer dimensions of a ddg_rope_tensor's x or y as (size, stride),
+// largest stride first; dimensions of size 1 count as stride 0.
+struct View {
+  const void* base;
+  int64_t n[3], st[3];
+};
+
+View rope_view(const ddg_rope_tensor& t, bool out, int64_t batch, int64_t tokens) {
+  return out ? View{t.y, {batch, tokens, t.heads}, {t.y_batch, t.y_token, t.y_head}}
+             : View{t.x, {batch, tokens, t.heads}, {t.x_batch, t.x_token, t.x_head}};
+}
+
+// Elements from the first to past the last of dims [d, 3) (in `order`) and a
+// head's values.
+int64_t extent(const View& v, const int* order, int d, int64_t dim) {
+  int64_t e = dim;
+  for (; d < 3; ++d) e += (v.n[order[d]] - 1) * v.st[order[d]];
+  return e;
+}
+
+void stride_order(const View& v, int* order) {
+  order[0] = 0; order[1] = 1; order[2] = 2;
+  auto key = [&](int d) { return v.n[d] > 1 ? v.st[d] : INT64_MAX; };
+  std::stable_sort(order, order + 3, [&](int p, int q) { return key(p) > key(q); });
+}
+
+// Every stride reaches past the dimensions below it: no element twice.
+bool nested(const View& v, int64_t dim) {
+  int order[3];
+  stride_order(v, order);
+  for (int d = 0; d < 3; ++d)
+    if (v.n[order[d]] > 1 && v.st[order[d]] < extent(v, order, d + 1, dim)) return false;
+  return true;
+}
+
+// No element of b, whose first value lies `delta` elements after a's, is one
+// of a's: dims [d, 3) of two nested views with the same strides and order.
+bool apart(const View& a, const View& b, const int* order, int d, int64_t delta, int64_t dim) {
+  while (d < 3 && a.n[order[d]] == 1 && b.n[order[d]] == 1) ++d;
+  if (delta >= extent(a, order, d, dim) || -delta >= extent(b, order, d, dim)) return true;
+  if (d == 3) return false;
+  const int64_t st = a.st[order[d]];
+  // entries i of a and j of b are delta + (j - i) st apart; past the two
+  // nearest multiples, whole inner extents lie between
+  const int64_t q = delta / st;
+  for (int64_t s = q - 1; s <= q + 1; ++s) {
+    const bool reached = s >= 0 ? s < a.n[order[d]] : -s < b.n[order[d]];
+    if (reached && !apart(a, b, order, d + 1, delta - s * st, dim)) return false;
+  }
+  return true;
+}
+
+bool same_view(const View& a, const View& b) {
+  if (a.base != b.base) return false;
+  for (int d = 0; d < 3; ++d)
+    if (a.n[d] != b.n[d] || (a.n[d] > 1 && a.st[d] != b.st[d])) return false;
+  return true;
+}
+
+// The views share no element, as far as the host can prove it: separate
+// address ranges, or interleaved views of the same strides.
+bool disjoint(View a, View b, int64_t dim, int size) {
+  const int none[3] = {0, 1, 2};
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.base), pb = reinterpret_cast<uintptr_t>(b.base);
+  const uintptr_t ea = (uintptr_t)extent(a, none, 0, dim) * size, eb = (uintptr_t)extent(b, none, 0, dim) * size;
+  if (pa + ea <= pb || pb + eb <= pa) return true;
+  for (int d = 0; d < 3; ++d) {
+    if (a.n[d] == 1) a.st[d] = b.st[d];
+    if (b.n[d] == 1) b.st[d] = a.st[d];
+    if (a.st[d] != b.st[d]) return false;
+  }
+  View both = a;
+  for (int d = 0; d < 3; ++d) both.n[d] = std::max(a.n[d], b.n[d]);
+  if (!nested(both, dim)) return false;
+  const int64_t delta = pb >= pa ? (int64_t)((pb - pa) / size) : -(int64_t)((pa - pb) / size);
+  if ((pb >= pa ? pb - pa : pa - pb) % size) return false;
+  int order[3];
+  stride_order(both, order);
+  return apart(a, b, order, 0, delta, dim);
+}
+
+// most elements that one dimension of a view reaches over (byte counts stay
+// well inside int64)
+constexpr int64_t kRopeMaxReach = INT64_C(1) << 58;
+
+int check_rope_tensor(const ddg_rope_tensor& t, int dtype, int weight_dtype, int64_t batch, int64_t tokens) {
+  if (t.heads < 1 || t.heads > DDG_ROPE_MAX_HEADS) return DDG_ERR_SHAPE;
+  const int64_t n[3] = {batch, tokens, t.heads};
+  const int64_t st[2][3] = {{t.x_batch, t.x_token, t.x_head}, {t.y_batch, t.y_token, t.y_head}};
+  for (int i = 0; i < 2; ++i)
+    for (int d = 0; d < 3; ++d)
+      if (st[i][d] < 0 || (n[d] > 1 && st[i][d] > kRopeMaxReach / n[d])) return DDG_ERR_SHAPE;
+  if (!t.x || !t.y) return DDG_ERR_ARG;
+  const uintptr_t es = dtype == DDG_F32 ? 4 : 2;
+  if (!aligned(t.x, es) || !aligned(t.y, es) || !aligned(t.weight, weight_dtype == DDG_F32 ? 4 : 2))
+    return DDG_ERR_ALIGN;
+  return DDG_OK;
+}
+
+int rope_call(const ddg_rope_tensor* q, const ddg_rope_tensor* k, int dtype, int weight_dtype, int64_t batch,
+              int64_t tokens, int head_dim, int norm, float eps, const ddg_rope_desc* rope, hipStream_t stream) {
+  if ((dtype != DDG_BF16 && dtype != DDG_F32) || (weight_dtype != DDG_BF16 && weight_dtype != DDG_F32) || !q || !rope)
+    return DDG_ERR_ARG;
+  if (!(eps >= 0.0f) || eps > 3.4e38f || !(std::fabs(rope->amplitude) <= 3.4e38f) ||
+      (rope->layout != DDG_ROPE_INTERLEAVED && rope->layout != DDG_ROPE_HALF) || (rope->inverse & ~1))
+    return DDG_ERR_ARG;
+  if (batch < 0 || tokens < 0 || (batch > 0 && tokens > kMaxDim / batch) || head_dim < 2 || head_dim % 2 ||
+      head_dim > DDG_ROPE_MAX_HEAD_DIM || rope->rot_dim < (norm == DDG_NORM_NONE ? 2 : 0) || rope->rot_dim % 2 ||
+      rope->rot_dim > head_dim)
+    return DDG_ERR_SHAPE;
+  if (rope->axes < 1 || rope->axes > DDG_ROPE_MAX_AXES || rope->positions_batch < 0 ||
+      rope->positions_batch > kRopeMaxReach / std::max<int64_t>(batch, 1))
+    return DDG_ERR_SHAPE;
+  ddg::RopeArgs a{};
+  int64_t sum = 0;
+  for (int i = 0; i < DDG_ROPE_MAX_AXES; ++i) {
+    if (i < rope->axes) {
+      if (rope->sections[i] < 0) return DDG_ERR_SHAPE;
+      sum += rope->sections[i];
+    }
+    a.ends[i] = i + 1 < rope->axes ? (int)std::min<int64_t>(sum, kMaxDim) : (int)kMaxDim;
+  }
+  if (sum != rope->rot_dim / 2) return DDG_ERR_SHAPE;
+  if (batch == 0 || tokens == 0) return DDG_OK;
+  if (rope->rot_dim > 0) {
+    if (!rope->positions || !rope->freqs) return DDG_ERR_ARG;
+    if (!aligned(rope->positions, 4) || !aligned(rope->freqs, 8)) return DDG_ERR_ALIGN;
+  }
+  const int size = dtype == DDG_F32 ? 4 : 2;
+  const ddg_rope_tensor* ts[2] = {q, k};
+  for (int i = 0; i < 2; ++i) {
+    if (!ts[i]) continue;
+    if (int st = check_rope_tensor(*ts[i], dtype, weight_dtype, batch, tokens)) return st;
+  }
+  for (int i = 0; i < 2; ++i) {
+    if (!ts[i]) continue;
+    const View y = rope_view(*ts[i], true, batch, tokens);
+    if (!nested(y, head_dim)) return DDG_ERR_ARG;
+    for (int j = 0; j < 2; ++j) {
+      if (!ts[j]) continue;
+      const View x = rope_view(*ts[j], false, batch, tokens);
+      if (!(i == j && same_view(x, y)) && !disjoint(x, y, head_dim, size)) return DDG_ERR_ARG;
+      if (i < j && !disjoint(y, rope_view(*ts[j], true, batch, tokens), head_dim, size)) return DDG_ERR_ARG;
+    }
+  }
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  auto fill = [](const ddg_rope_tensor* t) {
+    ddg::RopeTensor r{};
+    if (t)
+      r = ddg::RopeTensor{t->x, t->y, t->weight, t->x_batch, t->x_token, t->x_head,
+                          t->y_batch, t->y_token, t->y_head, (int)t->heads};
+    return r;
+  };
+  a.q = fill(q);
+  a.k = fill(k);
+  a.pos = rope->positions;
+  a.pos_batch = rope->positions_batch;
+  a.freqs = rope->freqs;
+  a.axes = rope->axes;
+  a.pairs = rope->rot_dim / 2;
+  a.dim = head_dim;
+  a.batch = (int)batch;
+  a.tokens = (int)tokens;
+  a.w_f32 = weight_dtype == DDG_F32;
+  a.eps = eps;
+  a.amplitude = rope->amplitude;
+  a.signed_amplitude = rope->inverse ? -rope->amplitude : rope->amplitude;
+  return hip_status(ddg::launch_rope(a, norm, rope->layout == DDG_ROPE_HALF, dtype == DDG_F32, cus, stream));
+}
+}  // namespace
+
+int ddg_rope(const ddg_rope_tensor* x, int dtype, int64_t batch, int64_t tokens, int head_dim,
+             const ddg_rope_desc* rope, hipStream_t stream) {
+  return rope_call(x, nullptr, dtype, DDG_F32, batch, tokens, head_dim, DDG_NORM_NONE, 0.0f, rope, stream);
+}
+
+int ddg_qk_norm_rope(const ddg_rope_tensor* q, const ddg_rope_tensor* k, int dtype, int weight_dtype,
+                     int64_t batch, int64_t tokens, int head_dim, int norm, float eps,
+                     const ddg_rope_desc* rope, hipStream_t stream) {
+  if (norm != DDG_NORM_HEAD && norm != DDG_NORM_TOKEN) return DDG_ERR_ARG;
+  return rope_call(q, k, dtype, weight_dtype, batch, tokens, head_dim, norm, eps, rope, stream);
 }
 
 namespace {

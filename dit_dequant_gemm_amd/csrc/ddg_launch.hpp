@@ -61,6 +61,32 @@ hipError_t launch_rpbh_rotate(const void* x, bool f32_in, int64_t n, int d, cons
                               const int8_t* signs, int h, void* out, bool f32_out, int cus,
                               hipStream_t stream);
 
+// Rotary positions of q (and, with k.heads > 0, k), behind a norm or alone.
+// Strides in elements; w: norm weights (head: dim values, token: heads x dim)
+// or null; ends: prefix sums of the axes' pair counts (INT_MAX from the last
+// axis on).
+constexpr int kRopeMaxAxes = 4;
+constexpr int kRopeMaxHeadDim = 512;
+struct RopeTensor {
+  const void* x;
+  void* y;
+  const void* w;
+  int64_t xb, xt, xh, yb, yt, yh;
+  int heads;
+};
+struct RopeArgs {
+  RopeTensor q, k;
+  const int32_t* pos;       // (token, axis) positions, pos_batch entries between batches
+  const double* freqs;      // radians per position of each pair
+  int64_t pos_batch;
+  int ends[kRopeMaxAxes];
+  int axes, pairs, dim, batch, tokens, w_f32;
+  float eps, amplitude, signed_amplitude;    // signed: negative for the inverse
+  int lg, splits;           // set by the launcher
+};
+// norm: DDG_NORM_*; half: the half layout
+hipError_t launch_rope(const RopeArgs& a, int norm, bool half, bool f32, int cus, hipStream_t stream);
+
 // FP4 weights x FP8 activations (formats: kFp4E2M1, kFp4E3M0, kFp4E1M2)
 constexpr int kFp4E2M1 = 0, kFp4E3M0 = 1, kFp4E1M2 = 2;
 struct W4A8Args {

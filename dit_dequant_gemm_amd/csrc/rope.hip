@@ -1,0 +1,508 @@
+// Rotary positions, alone or behind the norms of queries and keys.
+//
+// A head is a row x of D values.  Its first 2P values are P pairs (u, v):
+// (x[2p], x[2p+1]) in the interleaved layout, (x[p], x[P+p]) in the half
+// layout.  Pair p turns by the angle theta = pos[axis(p)] * freq[p]:
+//   (u, v) -> amplitude * (u cos theta - v sin theta, v cos theta + u sin theta),
+// the inverse by -theta; values from 2P on pass through.  With a norm, x is
+// first replaced by x * rsqrt(mean(x^2) + eps) * w, the mean over the head
+// or over all heads of the token.  Everything between the load and the one
+// rounding at the store is float32; the angle is float64 (a position of 10^6
+// times a frequency near 1 leaves float32 no fraction of a turn to speak of).
+//
+// Bound by HBM: each value is read and written once.  The sines and cosines
+// belong to a (token, pair) and not to a head, so a wave computes those of its
+// lanes' pairs once per token and keeps them in registers over the heads; no
+// table is read.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "ddg.h"
+#include "ddg_launch.hpp"
+
+namespace ddg {
+
+namespace {
+
+// cos and sin of 2 pi t: whole turns drop out in float64 and the rest is
+// taken to the nearest quarter turn, so that the Taylor sums below run over
+// at most pi/4 (their first dropped terms are 2e-9 of x for the sine and
+// 1e-10 for the cosine, under half an ulp of float32).
+__device__ __forceinline__ void cos_sin_turns(double t, float& c, float& s) {
+  t -= __builtin_rint(t);
+  const double q = __builtin_rint(4.0 * t);
+  const float x = (float)(__builtin_fma(-0.25, q, t) * 6.283185307179586477);
+  const float z = x * x;
+  float ps = __builtin_fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  ps = __builtin_fmaf(z, ps, 1.0f / 120.0f);
+  ps = __builtin_fmaf(z, ps, -1.0f / 6.0f);
+  const float sx = __builtin_fmaf(x * z, ps, x);
+  float pc = __builtin_fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  pc = __builtin_fmaf(z, pc, -1.0f / 720.0f);
+  pc = __builtin_fmaf(z, pc, 1.0f / 24.0f);
+  pc = __builtin_fmaf(z, pc, -0.5f);
+  const float cx = __builtin_fmaf(z, pc, 1.0f);
+  const int n = (int)q;                              // -2 .. 2 quarter turns
+  const float a = (n & 1) ? sx : cx, b = (n & 1) ? cx : sx;
+  c = ((n + 1) & 2) ? -a : a;
+  s = (n & 2) ? -b : b;
+}
+
+// Angle of pair p at the token whose positions start at pos, in turns.
+__device__ __forceinline__ double pair_turns(const RopeArgs& a, const int32_t* pos, int p) {
+  int axis = 0;
+#pragma unroll
+  for (int i = 0; i < kRopeMaxAxes - 1; ++i) axis += p >= a.ends[i] ? 1 : 0;
+  return (double)pos[axis] * (a.freqs[p] * 0.15915494309189533577);
+}
+
+// V consecutive values as float32 (the address is a multiple of their bytes).
+template <typename T, int V>
+__device__ __forceinline__ void load_vals(const void* base, int64_t i, float (&f)[V]) {
+  const T* p = static_cast<const T*>(base) + i;
+  if constexpr (sizeof(T) == 4 && V == 4) {
+    const f32x4 t = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = t[j];
+  } else if constexpr (sizeof(T) == 2 && V >= 4) {
+    uint32_t w[V / 2];
+    if constexpr (V == 8) {
+      const u32x4 t = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = t[j];
+    } else {
+      const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+      w[0] = t[0];
+      w[1] = t[1];
+    }
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      f[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
+      f[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = (float)p[j];
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vals(void* base, int64_t i, const float (&f)[V]) {
+  T* p = static_cast<T*>(base) + i;
+  if constexpr (sizeof(T) == 4 && V == 4) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+  } else if constexpr (sizeof(T) == 2 && V == 8) {
+    *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                         pack_bf16x2(f[6], f[7])};
+  } else if constexpr (sizeof(T) == 2 && V == 4) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) p[j] = (T)f[j];
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_weight(const void* w, bool w_f32, int64_t i, float (&f)[V]) {
+  if (w == nullptr) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = 1.0f;
+  } else if (w_f32) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = static_cast<const float*>(w)[i + j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = bf16_bits_to_f32(static_cast<const uint16_t*>(w)[i + j]);
+  }
+}
+
+// A slot is two chunks of V values of a head: chunk a and chunk b.  Slots
+// below P / V hold the rotated part: chunk a at V slot, chunk b P further on,
+// so that in the half layout the pairs are (a[j], b[j]) and in the
+// interleaved one lie inside the chunks (V = 1: the pair itself).  The other
+// slots hold the rest of the head, 2V values each.  P and D / 2 are multiples
+// of V.
+template <int V, bool HALF>
+struct Slot {
+  int ia, ib;
+  bool turns;
+  __device__ __forceinline__ Slot(const RopeArgs& a, int slot) {
+    turns = slot * V < a.pairs;
+    if (!turns) {
+      ia = slot * 2 * V;
+      ib = ia + V;
+    } else if (V == 1 && !HALF) {
+      ia = 2 * slot;
+      ib = ia + 1;
+    } else {
+      ia = slot * V;
+      ib = a.pairs + ia;
+    }
+  }
+  // the pair whose angle entry j of the slot's V angles is
+  __device__ __forceinline__ int pair(int slot, int j) const {
+    if (HALF || V == 1) return slot * V + j;
+    return j < V / 2 ? ia / 2 + j : ib / 2 + j - V / 2;
+  }
+};
+
+template <int V, bool HALF>
+__device__ __forceinline__ void turn_slot(float (&fa)[V], float (&fb)[V], const float (&c)[V], const float (&s)[V]) {
+  if constexpr (HALF || V == 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const float u = fa[j], v = fb[j];
+      fa[j] = __builtin_fmaf(u, c[j], -(v * s[j]));
+      fb[j] = __builtin_fmaf(v, c[j], u * s[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      const float u = fa[2 * j], v = fa[2 * j + 1];
+      fa[2 * j] = __builtin_fmaf(u, c[j], -(v * s[j]));
+      fa[2 * j + 1] = __builtin_fmaf(v, c[j], u * s[j]);
+      const float u2 = fb[2 * j], v2 = fb[2 * j + 1];
+      const float c2 = c[V / 2 + j], s2 = s[V / 2 + j];
+      fb[2 * j] = __builtin_fmaf(u2, c2, -(v2 * s2));
+      fb[2 * j + 1] = __builtin_fmaf(v2, c2, u2 * s2);
+    }
+  }
+}
+
+template <int M>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), M, 0xF, 0xF, true));
+}
+
+// Sum over each aligned run of 2^lg lanes, the same in all of them.  Once
+// the lanes of a quad (a half row) agree, a mirror adds the other quad (half).
+__device__ __forceinline__ float run_sum(float v, int lg) {
+  if (lg > 0) v = add_dpp<0xB1>(v);       // lane ^ 1
+  if (lg > 1) v = add_dpp<0x4E>(v);       // lane ^ 2
+  if (lg > 2) v = add_dpp<0x141>(v);      // half-row mirror
+  if (lg > 3) v = add_dpp<0x140>(v);      // row mirror
+  if (lg > 4) v += __shfl_xor(v, 16);
+  if (lg > 5) v += __shfl_xor(v, 32);
+  return v;
+}
+
+__device__ __forceinline__ float rstd_of(float sum, int count, float eps) {
+  return 1.0f / __builtin_sqrtf(sum / (float)count + eps);
+}
+
+constexpr int kRopeWaves = 4;
+
+// No norm, or the norm over each head.  A wave takes one token (or, with
+// splits > 1, one of `splits` shares of its heads): 2^lg lanes per head, one
+// slot per lane, 64 >> lg heads at a time, query heads first.  V = 1 gives a
+// head to the whole wave, up to NS slots per lane.
+template <typename T, int V, bool HALF, bool NORM>
+__global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) {
+  constexpr int NS = V == 1 ? kRopeMaxHeadDim / 128 : 1;
+  constexpr int U = V == 1 ? 1 : 2;                       // head groups in flight
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sl = lane & ((1 << a.lg) - 1), hl = lane >> a.lg, hpw = 64 >> a.lg;
+  const int slots = a.dim / (2 * V);
+  const int gq = (a.q.heads + hpw - 1) / hpw, gk = (a.k.heads + hpw - 1) / hpw, groups = gq + gk;
+  const int64_t total = (int64_t)a.batch * a.tokens * a.splits;
+  for (int64_t w = (int64_t)blockIdx.x * kRopeWaves + wave; w < total; w += (int64_t)gridDim.x * kRopeWaves) {
+    const int row = (int)(w / a.splits), part = (int)(w - (int64_t)row * a.splits);
+    const int b = row / a.tokens, t = row - b * a.tokens;
+    const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
+    float c[NS][V], s[NS][V];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int slot = sl + 64 * i;
+      const Slot<V, HALF> k(a, slot);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        c[i][j] = 1.0f;
+        s[i][j] = 0.0f;
+      }
+      if (slot < slots && k.turns) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          cos_sin_turns(pair_turns(a, pos, k.pair(slot, j)), c[i][j], s[i][j]);
+          c[i][j] *= a.amplitude;
+          s[i][j] *= a.signed_amplitude;
+        }
+      }
+    }
+    const int g0 = (int)((int64_t)part * groups / a.splits), g1 = (int)((int64_t)(part + 1) * groups / a.splits);
+    for (int g = g0; g < g1; g += U) {
+      float fa[U][NS][V], fb[U][NS][V];
+      bool ok[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool is_q = g + u < gq;
+        const RopeTensor& x = is_q ? a.q : a.k;
+        const int h = (g + u - (is_q ? 0 : gq)) * hpw + hl;
+        ok[u] = g + u < g1 && h < x.heads;
+        const int64_t base = (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const int slot = sl + 64 * i;
+          if (ok[u] && slot < slots) {
+            const Slot<V, HALF> k(a, slot);
+            load_vals<T, V>(x.x, base + k.ia, fa[u][i]);
+            load_vals<T, V>(x.x, base + k.ib, fb[u][i]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) fa[u][i][j] = fb[u][i][j] = 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool is_q = g + u < gq;
+        const RopeTensor& x = is_q ? a.q : a.k;
+        const int h = (g + u - (is_q ? 0 : gq)) * hpw + hl;
+        float rstd = 1.0f;
+        if constexpr (NORM) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+              sum = __builtin_fmaf(fa[u][i][j], fa[u][i][j], __builtin_fmaf(fb[u][i][j], fb[u][i][j], sum));
+          rstd = rstd_of(run_sum(sum, a.lg), a.dim, a.eps);
+        }
+        const int64_t base = (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const int slot = sl + 64 * i;
+          if (!ok[u] || slot >= slots) continue;
+          const Slot<V, HALF> k(a, slot);
+          if constexpr (NORM) {
+            float wa[V], wb[V];
+            load_weight<V>(x.w, a.w_f32, k.ia, wa);
+            load_weight<V>(x.w, a.w_f32, k.ib, wb);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              fa[u][i][j] = fa[u][i][j] * rstd * wa[j];
+              fb[u][i][j] = fb[u][i][j] * rstd * wb[j];
+            }
+          }
+          if (k.turns) turn_slot<V, HALF>(fa[u][i], fb[u][i], c[i], s[i]);
+          store_vals<T, V>(x.y, base + k.ia, fa[u][i]);
+          store_vals<T, V>(x.y, base + k.ib, fb[u][i]);
+        }
+      }
+    }
+  }
+}
+
+// The norm over all heads of a token: a workgroup takes one token, its lanes
+// the (head, slot) items in order; the sums of squares of q and of k are
+// joined through LDS in wave order, and the token's cosines and sines are
+// computed once into LDS.  The first kHold items of a lane stay in registers
+// between the two passes; later ones are read again (from the L2).
+constexpr int kRopeMaxWaves = 8;
+template <typename T, int V, bool HALF>
+__global__ __launch_bounds__(64 * kRopeMaxWaves) void rope_token_kernel(RopeArgs a) {
+  constexpr int kHold = V == 1 ? 4 : 2;
+  __shared__ float cs[2][kRopeMaxHeadDim / 2];
+  __shared__ float part[2][kRopeMaxWaves];
+  const int tid = threadIdx.x, n = blockDim.x, lane = tid & 63, wave = tid >> 6, waves = n >> 6;
+  const int slots = a.dim / (2 * V);
+  for (int64_t row = blockIdx.x; row < (int64_t)a.batch * a.tokens; row += gridDim.x) {
+    const int b = (int)(row / a.tokens), t = (int)(row - (int64_t)b * a.tokens);
+    const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
+    float fa[2][kHold][V], fb[2][kHold][V];
+    float sum[2] = {0.0f, 0.0f};
+    auto load_item = [&](const RopeTensor& x, int item, float (&va)[V], float (&vb)[V]) {
+      const int h = item / slots, slot = item - h * slots;
+      const Slot<V, HALF> k(a, slot);
+      const int64_t base = (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
+      load_vals<T, V>(x.x, base + k.ia, va);
+      load_vals<T, V>(x.x, base + k.ib, vb);
+    };
+    auto finish_item = [&](const RopeTensor& x, int item, float rstd, float (&va)[V], float (&vb)[V]) {
+      const int h = item / slots, slot = item - h * slots;
+      const Slot<V, HALF> k(a, slot);
+      float wa[V], wb[V];
+      load_weight<V>(x.w, a.w_f32, (int64_t)h * a.dim + k.ia, wa);
+      load_weight<V>(x.w, a.w_f32, (int64_t)h * a.dim + k.ib, wb);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        va[j] = va[j] * rstd * wa[j];
+        vb[j] = vb[j] * rstd * wb[j];
+      }
+      if (k.turns) {
+        float c[V], s[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int p = k.pair(slot, j);
+          c[j] = cs[0][p];
+          s[j] = cs[1][p];
+        }
+        turn_slot<V, HALF>(va, vb, c, s);
+      }
+      const int64_t base = (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh;
+      store_vals<T, V>(x.y, base + k.ia, va);
+      store_vals<T, V>(x.y, base + k.ib, vb);
+    };
+    auto squares = [&](const float (&va)[V], const float (&vb)[V], float acc) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc = __builtin_fmaf(va[j], va[j], __builtin_fmaf(vb[j], vb[j], acc));
+      return acc;
+    };
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const RopeTensor& x = z ? a.k : a.q;
+      const int items = x.heads * slots;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) {
+        const int item = tid + i * n;
+        if (item < items) load_item(x, item, fa[z][i], fb[z][i]);
+      }
+    }
+    for (int p = tid; p < a.pairs; p += n) {
+      float c, s;
+      cos_sin_turns(pair_turns(a, pos, p), c, s);
+      cs[0][p] = c * a.amplitude;
+      cs[1][p] = s * a.signed_amplitude;
+    }
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const RopeTensor& x = z ? a.k : a.q;
+      const int items = x.heads * slots;
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (tid + i * n < items) sum[z] = squares(fa[z][i], fb[z][i], sum[z]);
+      for (int item = tid + kHold * n; item < items; item += n) {
+        float va[V], vb[V];
+        load_item(x, item, va, vb);
+        sum[z] = squares(va, vb, sum[z]);
+      }
+      sum[z] = run_sum(sum[z], 6);
+      if (lane == 0) part[z][wave] = sum[z];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const RopeTensor& x = z ? a.k : a.q;
+      const int items = x.heads * slots;
+      float all = 0.0f;
+      for (int i = 0; i < waves; ++i) all += part[z][i];
+      const float rstd = rstd_of(all, x.heads * a.dim, a.eps);
+#pragma unroll
+      for (int i = 0; i < kHold; ++i)
+        if (tid + i * n < items) finish_item(x, tid + i * n, rstd, fa[z][i], fb[z][i]);
+      for (int item = tid + kHold * n; item < items; item += n) {
+        float va[V], vb[V];
+        load_item(x, item, va, vb);
+        finish_item(x, item, rstd, va, vb);
+      }
+    }
+    __syncthreads();                       // cs and part are free for the next token
+  }
+}
+
+template <typename T, int V, bool HALF>
+hipError_t launch_v(RopeArgs a, int norm, int cus, hipStream_t stream) {
+  const int slots = a.dim / (2 * V);
+  const int64_t rows = (int64_t)a.batch * a.tokens;
+  if (norm == DDG_NORM_TOKEN) {
+    // lanes in whole waves, the same number of items for nearly all of them
+    const int64_t items = (int64_t)std::max(a.q.heads, a.k.heads) * slots;
+    const int64_t per = (items + 64 * kRopeMaxWaves - 1) / (64 * kRopeMaxWaves);
+    const int lanes = (int)(((items + per - 1) / per + 63) / 64 * 64);
+    const int64_t grid = std::min<int64_t>(rows, (int64_t)cus * 64);
+    rope_token_kernel<T, V, HALF><<<dim3((unsigned)grid), dim3((unsigned)lanes), 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  a.lg = 0;
+  while ((1 << a.lg) < slots && a.lg < 6) ++a.lg;
+  const int hpw = 64 >> a.lg;
+  const int groups = (a.q.heads + hpw - 1) / hpw + (a.k.heads + hpw - 1) / hpw;
+  // a token's heads go to several waves while tokens alone leave waves idle
+  const int64_t want = (int64_t)cus * 16;
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(groups, want / rows));
+  const int64_t waves = rows * a.splits;
+  const int64_t grid = std::min<int64_t>((waves + kRopeWaves - 1) / kRopeWaves, (int64_t)cus * 64);
+  if (norm == DDG_NORM_HEAD)
+    rope_head_kernel<T, V, HALF, true><<<dim3((unsigned)grid), dim3(64 * kRopeWaves), 0, stream>>>(a);
+  else
+    rope_head_kernel<T, V, HALF, false><<<dim3((unsigned)grid), dim3(64 * kRopeWaves), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int V>
+hipError_t launch_layout(const RopeArgs& a, int norm, bool half, int cus, hipStream_t stream) {
+  return half ? launch_v<T, V, true>(a, norm, cus, stream) : launch_v<T, V, false>(a, norm, cus, stream);
+}
+
+// Chunks of V values are aligned in every row of x, and split the head.
+bool chunks_of(const RopeArgs& a, int es, int v) {
+  if (a.dim % (2 * v) || a.pairs % v) return false;
+  auto ok = [&](const RopeTensor& x) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(x.x) | reinterpret_cast<uintptr_t>(x.y);
+    const int64_t st = x.xb | x.xt | x.xh | x.yb | x.yt | x.yh;
+    return x.heads == 0 || (at % (uintptr_t)(v * es) == 0 && st % v == 0);
+  };
+  return ok(a.q) && ok(a.k);
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs& a, int norm, bool half, bool f32, int cus, hipStream_t stream) {
+  // the widest chunks that the head, the rotated part and the rows allow
+  if (f32) {
+    if (chunks_of(a, 4, 4)) return launch_layout<float, 4>(a, norm, half, cus, stream);
+    return launch_layout<float, 1>(a, norm, half, cus, stream);
+  }
+  if (chunks_of(a, 2, 8)) return launch_layout<__bf16, 8>(a, norm, half, cus, stream);
+  if (chunks_of(a, 2, 4)) return launch_layout<__bf16, 4>(a, norm, half, cus, stream);
+  return launch_layout<__bf16, 1>(a, norm, half, cus, stream);
+}
+
+}  // namespace ddg
+
+// Host only.  Pair i of `rot` values turns freq_i = base^(-2i / rot) per
+// position; the scalings for contexts `factor` times the original length:
+//   linear  freq_i / factor (positions interpolated);
+//   ntk     base * factor^(rot / (rot - 2)): the first pair keeps its
+//           frequency, the last one gets freq / factor;
+//   yarn    pairs that turn at least beta_fast times over the original length
+//           keep their frequency, those under beta_slow turns are divided by
+//           factor, with a linear ramp over the pair index between; amplitude
+//           0.1 ln(factor) + 1.
+extern "C" int ddg_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_length,
+                                    double beta_fast, double beta_slow, double* freqs, double* amplitude) {
+  if (scaling < DDG_ROPE_SCALE_NONE || scaling > DDG_ROPE_SCALE_YARN || !freqs || !amplitude) return DDG_ERR_ARG;
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > DDG_ROPE_MAX_HEAD_DIM) return DDG_ERR_SHAPE;
+  if (!(base > 1.0) || !std::isfinite(base)) return DDG_ERR_ARG;
+  if (scaling != DDG_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return DDG_ERR_ARG;
+  if (scaling == DDG_ROPE_SCALE_NTK && rot_dim < 4) return DDG_ERR_SHAPE;
+  if (scaling == DDG_ROPE_SCALE_YARN &&
+      (!(original_length >= 1.0) || !std::isfinite(original_length) || !(beta_slow > 0.0) ||
+       !(beta_fast >= beta_slow) || !std::isfinite(beta_fast)))
+    return DDG_ERR_ARG;
+  const int pairs = rot_dim / 2;
+  const double b = scaling == DDG_ROPE_SCALE_NTK ? base * std::pow(factor, rot_dim / (rot_dim - 2.0)) : base;
+  double low = 0.0, high = 0.0;
+  if (scaling == DDG_ROPE_SCALE_YARN) {
+    // pair index whose wavelength fits `turns` times into the original length
+    auto pair_of = [&](double turns) {
+      return rot_dim * std::log(original_length / (turns * 2.0 * M_PI)) / (2.0 * std::log(base));
+    };
+    low = std::max(std::floor(pair_of(beta_fast)), 0.0);
+    high = std::min(std::ceil(pair_of(beta_slow)), rot_dim - 1.0);
+  }
+  for (int i = 0; i < pairs; ++i) {
+    const double f = std::pow(b, -2.0 * i / rot_dim);
+    if (scaling == DDG_ROPE_SCALE_LINEAR) {
+      freqs[i] = f / factor;
+    } else if (scaling == DDG_ROPE_SCALE_YARN) {
+      const double ramp = std::min(std::max((i - low) / std::max(high - low, 0.001), 0.0), 1.0);
+      freqs[i] = f * (1.0 - ramp) + f / factor * ramp;
+    } else {
+      freqs[i] = f;
+    }
+  }
+  *amplitude = scaling == DDG_ROPE_SCALE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return DDG_OK;
+}

@@ -365,6 +365,112 @@ int ddg_rpbh_rotate(const void* x, int x_dtype, int64_t n, int64_t d, const int3
                     const int8_t* signs, int h, void* out, int out_dtype, hipStream_t stream);
 
 /*
+ * Rotary positions, and the norms of queries and keys with the rotation in
+ * the same pass: the rows between a block's q and k projections and its
+ * attention.
+ *
+ * A tensor is batch x tokens x heads x head_dim values (ddg_rope_tensor): the
+ * head_dim values of a head are consecutive, the other strides free (slices
+ * of a fused projection's output, head-major copies).  The first rot_dim = 2P
+ * values of a head are P pairs (u, v), (x[2p], x[2p+1]) with
+ * DDG_ROPE_INTERLEAVED or (x[p], x[P+p]) with DDG_ROPE_HALF; pair p of a
+ * token turns by theta = position[axis(p)] * freqs[p] (float64):
+ *   u' = amplitude (u cos theta - v sin theta)
+ *   v' = amplitude (v cos theta + u sin theta),
+ * by -theta with `inverse` (its transpose: the rotation's gradient, for
+ * amplitude 1 also its inverse).  Values from rot_dim on pass through.  All
+ * arithmetic is float32 up to one rounding at the store.
+ */
+#define DDG_ROPE_MAX_HEAD_DIM 512
+#define DDG_ROPE_MAX_AXES 4
+#define DDG_ROPE_MAX_HEADS 65535
+#define DDG_ROPE_INTERLEAVED 0
+#define DDG_ROPE_HALF 1
+#define DDG_NORM_NONE 0
+#define DDG_NORM_HEAD 1     /* mean of squares over each head                */
+#define DDG_NORM_TOKEN 2    /* ... over all heads of a token                 */
+
+typedef struct ddg_rope_tensor {
+  const void* x;            /* aligned to its element                        */
+  void* y;                  /* may be x itself, with x's strides             */
+  const void* weight;       /* norm weights: head_dim values (DDG_NORM_HEAD) */
+                            /* or heads * head_dim (DDG_NORM_TOKEN); NULL: 1 */
+  int64_t heads;
+  int64_t x_batch, x_token, x_head;   /* strides in elements, >= 0           */
+  int64_t y_batch, y_token, y_head;
+} ddg_rope_tensor;
+
+typedef struct ddg_rope_desc {
+  const int32_t* positions; /* device: (token, axis) row-major               */
+  int64_t positions_batch;  /* entries from one batch's positions to the     */
+                            /* next; 0: all batches share one set            */
+  const double* freqs;      /* device, rot_dim / 2: radians per position     */
+  int axes;                 /* 1..DDG_ROPE_MAX_AXES                          */
+  int sections[DDG_ROPE_MAX_AXES];    /* pairs of each axis, in order; their */
+                            /* sum is rot_dim / 2                            */
+  int rot_dim;              /* even, at most head_dim                        */
+  int layout;               /* DDG_ROPE_INTERLEAVED or DDG_ROPE_HALF         */
+  int inverse;              /* 0 or 1                                        */
+  float amplitude;          /* factor of the rotated values (1: none)        */
+} ddg_rope_desc;
+
+/*
+ * y = the rotation of x.
+ * batch or tokens == 0 is a no-op.  Errors: DDG_ERR_ARG (null pointer, dtype,
+ * layout, inverse, non-finite amplitude; y's elements overlap one another, or
+ * x's without being the same view), DDG_ERR_SHAPE (batch or tokens negative
+ * or batch * tokens above 2^31 - 1; heads outside 1..DDG_ROPE_MAX_HEADS;
+ * head_dim odd or outside 2..DDG_ROPE_MAX_HEAD_DIM; rot_dim odd or outside
+ * 2..head_dim; axes, sections; a stride negative or, times its dimension,
+ * above 2^58), DDG_ERR_ALIGN (x, y or a
+ * weight not aligned to an element, positions to 4 bytes, freqs to 8),
+ * DDG_ERR_HIP, DDG_ERR_UNSUPPORTED.  Two views of one buffer whose strides
+ * agree (slices of a fused projection) may interleave; other views must lie
+ * in separate ranges.
+ */
+int ddg_rope(const ddg_rope_tensor* x, int dtype, int64_t batch, int64_t tokens, int head_dim,
+             const ddg_rope_desc* rope, hipStream_t stream);
+
+/*
+ * Root-mean-square norms of q and of k, then the rotation:
+ *   n = x * rsqrt(mean(x^2) + eps) * weight, y = rotation(n),
+ * the mean and its square root in float32 (a row whose squares overflow
+ * float32 gives the limit of that arithmetic; a zero row with eps = 0 gives
+ * NaN).  norm: DDG_NORM_HEAD or DDG_NORM_TOKEN.  q and k have separate head
+ * counts; k may be NULL.  weight_dtype: DDG_BF16 or DDG_F32, both weights.
+ * rope->rot_dim may be 0 here (the norm alone; positions and freqs unused).
+ * Errors: as ddg_rope, with norm, weight_dtype and eps (finite, >= 0) under
+ * DDG_ERR_ARG, and each output checked against both inputs and the other
+ * output (in place: each output may be its own input).
+ */
+int ddg_qk_norm_rope(const ddg_rope_tensor* q, const ddg_rope_tensor* k, int dtype, int weight_dtype,
+                     int64_t batch, int64_t tokens, int head_dim, int norm, float eps,
+                     const ddg_rope_desc* rope, hipStream_t stream);
+
+/*
+ * Frequencies of the rotation, and their scalings for contexts `factor` times
+ * longer than original_length.  Host only (host pointers, nothing runs on the
+ * GPU).  freqs <- rot_dim / 2 values, freq_i = base^(-2i / rot_dim), then
+ *   DDG_ROPE_SCALE_LINEAR  freq_i / factor;
+ *   DDG_ROPE_SCALE_NTK     base replaced by base * factor^(rot_dim / (rot_dim - 2));
+ *   DDG_ROPE_SCALE_YARN    with i(n) = rot_dim ln(original_length / (2 pi n)) / (2 ln base),
+ *                          low = max(floor(i(beta_fast)), 0),
+ *                          high = min(ceil(i(beta_slow)), rot_dim - 1) and
+ *                          r = clamp((i - low) / max(high - low, 0.001), 0, 1):
+ *                          freq_i (1 - r) + freq_i / factor * r.
+ * amplitude <- 0.1 ln(factor) + 1 for YARN, else 1.
+ * Errors: DDG_ERR_ARG (null pointer, scaling, base not above 1, factor below 1,
+ * YARN's lengths and turn counts), DDG_ERR_SHAPE (rot_dim odd or outside
+ * 2..DDG_ROPE_MAX_HEAD_DIM; below 4 with NTK).
+ */
+#define DDG_ROPE_SCALE_NONE 0
+#define DDG_ROPE_SCALE_LINEAR 1
+#define DDG_ROPE_SCALE_NTK 2
+#define DDG_ROPE_SCALE_YARN 3
+int ddg_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_length,
+                         double beta_fast, double beta_slow, double* freqs, double* amplitude);
+
+/*
  * FP4 weights and FP8 activations (W4A8), the FP4DiT article: 4-bit
  * floating-point weight formats in groups of 128 (§3.2.1, §4.1) and 8-bit
  * per-token activations (§3.2.3), multiplied on the gfx950 scaled matrix
