@@ -69,6 +69,9 @@ SIGNATURES = {
                                         _c_int, _vp, _c_int, _vp, _sz, _vp]),
     "ddg_lowrank_fused_gemm_noalloc": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _c_int, _c_i64, _vp, _vp,
                                                 _c_int, _vp, _c_int, _vp]),
+    "ddg_adapter_gemm": (_c_int, [_vp, _c_i64, _c_i64, _vp, _vp, _c_int, _c_i64, _vp, _vp, _vp, _c_i64, _c_int, _vp,
+                                  _vp, _c_int, _vp, _sz, _vp]),
+    "ddg_adapter_workspace_bytes": (_c_int, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, ctypes.POINTER(_sz)]),
     "ddg_rpbh_rotate": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _vp, _c_int, _vp, _c_int, _vp]),
     "ddg_rope": (_c_int, [ctypes.POINTER(RopeTensor), _c_int, _c_i64, _c_i64, _c_int, ctypes.POINTER(RopeDesc), _vp]),
     "ddg_qk_norm_rope": (_c_int, [ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor), _c_int, _c_int, _c_i64,
@@ -709,6 +712,92 @@ def lowrank_fused_gemm_noalloc(x: torch.Tensor, qw: QWeight, lora_down: torch.Te
         DDG_F32 if out.dtype == torch.float32 else DDG_BF16, _stream_ptr(x.device)),
         "ddg_lowrank_fused_gemm_noalloc")
     return out
+
+
+# ------------------------------------------------------------------ adapters of many requests
+class AdapterPool:
+    """Low-rank adapters of one projection, all of one rank: down (adapters x
+    r x in), up (adapters x out x r), both bf16, and scales (adapters,
+    float32).  r is a multiple of 8 within 8..128; smaller adapters are padded
+    with zeros (see stack)."""
+
+    def __init__(self, down: torch.Tensor, up: torch.Tensor, scales: torch.Tensor):
+        for t, name in ((down, "down"), (up, "up"), (scales, "scales")):
+            _require_cuda(t, name)
+        if down.dim() != 3 or up.dim() != 3 or down.dtype != torch.bfloat16 or up.dtype != torch.bfloat16:
+            raise ValueError("down and up must be 3-D bf16 tensors (adapters x r x in, adapters x out x r)")
+        if scales.dtype != torch.float32 or scales.shape != down.shape[:1]:
+            raise ValueError("scales must hold one float32 per adapter")
+        if up.shape[0] != down.shape[0] or up.shape[2] != down.shape[1]:
+            raise ValueError("down and up disagree in their adapters or rank")
+        if down.device != up.device or down.device != scales.device:
+            raise ValueError("down, up and scales must be on one device")
+        self.down, self.up, self.scales = down, up, scales
+
+    @classmethod
+    def stack(cls, adapters, qw: QWeight) -> "AdapterPool":
+        """A pool of separate (down r_i x in, up out x r_i, scale) adapters for
+        weight qw: ranks padded with zeros to the largest (a multiple of 8),
+        inputs to the record's padded input dimension."""
+        adapters = list(adapters)
+        if not adapters:
+            raise ValueError("no adapters")
+        r = max(8, -(-max(d.shape[0] for d, _, _ in adapters) // 8) * 8)
+        dev = adapters[0][0].device
+        down = torch.zeros(len(adapters), r, qw.k, dtype=torch.bfloat16, device=dev)
+        up = torch.zeros(len(adapters), qw.n, r, dtype=torch.bfloat16, device=dev)
+        for i, (d, u, _) in enumerate(adapters):
+            if d.dim() != 2 or u.dim() != 2 or d.shape[1] not in (qw.k, qw.orig_in) or u.shape != (qw.n, d.shape[0]):
+                raise ValueError(f"adapter {i}: down must be (r x in) and up (out x r)")
+            down[i, :d.shape[0], :d.shape[1]] = d
+            up[i, :, :d.shape[0]] = u
+        scales = torch.tensor([float(s) for _, _, s in adapters], dtype=torch.float32, device=dev)
+        return cls(down, up, scales)
+
+
+def adapter_workspace_bytes(m: int, n: int, k: int, r: int, split: bool = True) -> int:
+    """Workspace bytes of adapter_gemm (split False: the required part alone)."""
+    b = ctypes.c_size_t()
+    _check(load_library().ddg_adapter_workspace_bytes(m, n, k, r, int(split), ctypes.byref(b)),
+           "ddg_adapter_workspace_bytes")
+    return b.value
+
+
+def adapter_gemm(x: torch.Tensor, qw: QWeight, pool: AdapterPool, rows: torch.Tensor, out_dtype=torch.bfloat16,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y[i] = X[i] @ w_hat^T + s_a (X[i] @ down[a]^T) @ up[a]^T with a = rows[i]
+    (int32; a value outside the pool: no adapter), rows of many requests beside
+    one quantized weight.  workspace: optional scratch (uint8, at least
+    adapter_workspace_bytes(m, n, k, r, False) bytes, for split K with True);
+    by default each call takes its own from torch's allocator.  Under graph
+    capture K is not split (see dequant_gemm)."""
+    x = _prep_x(x, qw)
+    _require_cuda(rows, "rows")
+    m, r = x.shape[0], pool.down.shape[1]
+    if rows.dtype != torch.int32 or rows.shape != (m,):
+        raise ValueError("rows must be int32, one entry per row of x")
+    if pool.down.shape[2] != qw.k or pool.up.shape[1] != qw.n:
+        raise ValueError("the pool does not fit the weight")
+    y = _out(x, qw.n, out_dtype, out)
+    for t in (rows, pool.down, qw.packed, qw.scales, y):
+        if t.device != x.device:
+            raise ValueError("every tensor must be on the device of x")
+    with _device_of(x):
+        split = not _capturing()
+        if workspace is None:
+            workspace = torch.empty(max(256, adapter_workspace_bytes(m, qw.n, qw.k, r, split)), dtype=torch.uint8,
+                                    device=x.device)
+        else:
+            _require_cuda(workspace, "workspace")
+        wbytes = workspace.numel() * workspace.element_size()
+        if not split:
+            wbytes = min(wbytes, adapter_workspace_bytes(m, qw.n, qw.k, r, False))
+        _check(load_library().ddg_adapter_gemm(
+            x.data_ptr(), m, qw.k, qw.packed.data_ptr(), qw.scales.data_ptr(), qw.bits, qw.n, pool.down.data_ptr(),
+            pool.up.data_ptr(), pool.scales.data_ptr(), pool.down.shape[0], r, rows.data_ptr(), y.data_ptr(),
+            DDG_F32 if y.dtype == torch.float32 else DDG_BF16, workspace.data_ptr(), wbytes,
+            _stream_ptr(x.device)), "ddg_adapter_gemm")
+    return y
 
 
 # ------------------------------------------------------------------ bit allocation

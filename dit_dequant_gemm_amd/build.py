@@ -40,6 +40,7 @@ COMMON = [
 
 def _units():
     units = [(os.path.join(CSRC, "inst_bits.hip"), f"inst_b{b}", [f"-DDDG_BITS={b}"]) for b in BITS]
+    units += [(os.path.join(CSRC, "adapters.hip"), f"adapters_b{b}", [f"-DDDG_BITS={b}"]) for b in BITS]
     units.append((os.path.join(CSRC, "lowrank.hip"), "lowrank", []))
     units.append((os.path.join(CSRC, "grouped.hip"), "grouped", []))
     units.append((os.path.join(CSRC, "pd.hip"), "pd", []))

@@ -1,0 +1,112 @@
+// The products with per-row adapters for one bit width, DDG_BITS, and (in the
+// unit of width 4) the launcher of their pre-pass.  Compiled once per width.
+#include "ddg_launch.hpp"
+
+#ifndef DDG_BITS
+#error "compile with -DDDG_BITS=<3..7>"
+#endif
+
+namespace ddg {
+
+template <>
+hipError_t launch_adapter_large<DDG_BITS>(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
+  gemm_large_adapter_kernel<DDG_BITS><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), 0, stream>>>(a, ad);
+  return hipGetLastError();
+}
+
+template <>
+hipError_t launch_adapter_n192<DDG_BITS>(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream) {
+  gemm_n192_adapter_kernel<DDG_BITS><<<dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, stream>>>(a, ad);
+  return hipGetLastError();
+}
+
+template <>
+hipError_t launch_adapter_streamk<DDG_BITS>(const GemmArgs& a, const StreamK& sk, int grid, const AdapterArgs& ad,
+                                            hipStream_t stream) {
+  gemm_streamk_kernel<DDG_BITS><<<dim3((unsigned)grid), dim3(512), 0, stream>>>(a, sk, ad);
+  return hipGetLastError();
+}
+
+template <>
+hipError_t launch_adapter_small<DDG_BITS>(const GemmArgs& a, int rb, int nc, int nk, const AdapterArgs& ad,
+                                          hipStream_t stream) {
+  const dim3 grid((unsigned)((a.n + 16 * nc - 1) / (16 * nc)));
+#define DDG_SMALL(RB, NC, NK)                                                                         \
+  if (rb == RB && nc == NC && nk == NK) {                                                             \
+    gemm_small_adapter_kernel<DDG_BITS, RB, NC, NK><<<grid, dim3(64 * NC * NK), 0, stream>>>(a, ad); \
+    return hipGetLastError();                                                                         \
+  }
+  DDG_SMALL(1, 1, 8) DDG_SMALL(1, 2, 4) DDG_SMALL(1, 4, 2)
+  DDG_SMALL(2, 1, 4) DDG_SMALL(2, 2, 2)
+  DDG_SMALL(4, 1, 4) DDG_SMALL(4, 2, 2)
+#undef DDG_SMALL
+  return hipErrorInvalidValue;
+}
+
+template <>
+hipError_t launch_adapter_small_split<DDG_BITS>(const GemmArgs& a, int nc, const SmallSplit& sp,
+                                                const AdapterArgs& ad, hipStream_t stream) {
+  if (sp.parts < 2 || sp.parts > kSmallMaxParts || nc != 2) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((a.n + 16 * nc - 1) / (16 * nc) * sp.parts));
+  gemm_small_split_adapter_kernel<DDG_BITS, 2><<<grid, dim3(128), 0, stream>>>(a, sp, ad);
+  return hipGetLastError();
+}
+
+template <>
+hipError_t launch_adapter_skinny<DDG_BITS>(const GemmArgs& a, int kc, int ncb, const AdapterArgs& ad,
+                                           hipStream_t stream) {
+  const dim3 grid((unsigned)((a.n + 16 * ncb - 1) / (16 * ncb)));
+  if (skinny_static_lds(DDG_BITS, kc, ncb) + skinny_scale_lds(kc) > kLdsLimit) return hipErrorInvalidValue;
+#define DDG_SKINNY(KC, NCB)                                                                 \
+  if (kc == KC && ncb == NCB) {                                                             \
+    gemm_skinny_adapter_kernel<DDG_BITS, KC, NCB><<<grid, dim3(512), 0, stream>>>(a, ad);  \
+    return hipGetLastError();                                                               \
+  }
+  DDG_SKINNY(3, 1) DDG_SKINNY(3, 2) DDG_SKINNY(3, 4)
+  DDG_SKINNY(4, 1) DDG_SKINNY(4, 2) DDG_SKINNY(4, 4)
+  DDG_SKINNY(5, 1) DDG_SKINNY(5, 2) DDG_SKINNY(5, 4)
+#undef DDG_SKINNY
+  return hipErrorInvalidValue;
+}
+
+#if DDG_BITS == 4
+namespace {
+template <int RBLK, int RR>
+hipError_t launch_rr(const AdapterDown& d, int z, hipStream_t stream) {
+  const dim3 grid((unsigned)((d.m + 16 * RR - 1) / (16 * RR)), (unsigned)d.chunks, (unsigned)z);
+  adapter_down_kernel<RBLK, RR><<<grid, dim3(64 * kAdapterWaves), 0, stream>>>(d.x, d.down, d.scales, d.rows, d.count,
+                                                                             d.t, d.m, d.k, d.r, d.gpc);
+  return hipGetLastError();
+}
+
+template <int RBLK>
+hipError_t launch_rblk(const AdapterDown& d, int rr, int z, hipStream_t stream) {
+  if constexpr (RBLK <= 2) {
+    if (rr == 4) return launch_rr<RBLK, 4>(d, z, stream);
+  }
+  if constexpr (RBLK <= 4) {
+    if (rr == 2) return launch_rr<RBLK, 2>(d, z, stream);
+  }
+  return launch_rr<RBLK, 1>(d, z, stream);
+}
+}  // namespace
+
+hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream) {
+  const int rr = lowrank_t_row_blocks(d.m, d.r);
+  // few rows: the distinct adapters of a row block go to four workgroups
+  const int z = d.m <= 64 ? 4 : 1;
+  switch ((d.r + 15) / 16) {
+    case 1: return launch_rblk<1>(d, rr, z, stream);
+    case 2: return launch_rblk<2>(d, rr, z, stream);
+    case 3: return launch_rblk<3>(d, rr, z, stream);
+    case 4: return launch_rblk<4>(d, rr, z, stream);
+    case 5: return launch_rblk<5>(d, rr, z, stream);
+    case 6: return launch_rblk<6>(d, rr, z, stream);
+    case 7: return launch_rblk<7>(d, rr, z, stream);
+    case 8: return launch_rblk<8>(d, rr, z, stream);
+    default: return hipErrorInvalidValue;
+  }
+}
+#endif
+
+}  // namespace ddg

@@ -81,27 +81,37 @@ struct DequantizeF {
 template <int B>
 struct LargeF {
   template <typename... A>
-  static hipError_t run(A... a) { return ddg::launch_gemm_large<B>(a...); }
+  static hipError_t run(const ddg::AdapterArgs* ad, hipStream_t stream, A... a) {
+    return ad ? ddg::launch_adapter_large<B>(a..., *ad, stream) : ddg::launch_gemm_large<B>(a..., stream);
+  }
 };
 template <int B>
 struct N192F {
   template <typename... A>
-  static hipError_t run(A... a) { return ddg::launch_gemm_n192<B>(a...); }
+  static hipError_t run(const ddg::AdapterArgs* ad, hipStream_t stream, A... a) {
+    return ad ? ddg::launch_adapter_n192<B>(a..., *ad, stream) : ddg::launch_gemm_n192<B>(a..., stream);
+  }
 };
 template <int B>
 struct SmallSplitF {
   template <typename... A>
-  static hipError_t run(A... a) { return ddg::launch_gemm_small_split<B>(a...); }
+  static hipError_t run(const ddg::AdapterArgs* ad, hipStream_t stream, A... a) {
+    return ad ? ddg::launch_adapter_small_split<B>(a..., *ad, stream) : ddg::launch_gemm_small_split<B>(a..., stream);
+  }
 };
 template <int B>
 struct SkinnyF {
   template <typename... A>
-  static hipError_t run(A... a) { return ddg::launch_gemm_skinny<B>(a...); }
+  static hipError_t run(const ddg::AdapterArgs* ad, hipStream_t stream, A... a) {
+    return ad ? ddg::launch_adapter_skinny<B>(a..., *ad, stream) : ddg::launch_gemm_skinny<B>(a..., stream);
+  }
 };
 template <int B>
 struct SmallF {
   template <typename... A>
-  static hipError_t run(A... a) { return ddg::launch_gemm_small<B>(a...); }
+  static hipError_t run(const ddg::AdapterArgs* ad, hipStream_t stream, A... a) {
+    return ad ? ddg::launch_adapter_small<B>(a..., *ad, stream) : ddg::launch_gemm_small<B>(a..., stream);
+  }
 };
 
 // Validation shared by the two GEMM entry points.
@@ -134,7 +144,9 @@ int skinny_chunk(int g) {
 template <int B>
 struct StreamKF {
   template <typename... A>
-  static hipError_t run(A... a) { return ddg::launch_gemm_streamk<B>(a...); }
+  static hipError_t run(const ddg::AdapterArgs* ad, hipStream_t stream, A... a) {
+    return ad ? ddg::launch_adapter_streamk<B>(a..., *ad, stream) : ddg::launch_gemm_streamk<B>(a..., stream);
+  }
 };
 
 // Stream-K for the large-M product: one workgroup per compute unit, at most
@@ -238,8 +250,10 @@ struct Scratch {
   size_t bytes = 0;
 };
 
-// Kernel choice for the product; fills a.tiles_* for the large kernel.
-hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratch sk = {}, int cus = 0) {
+// Kernel choice for the product (with the rows' adapters when ad is set);
+// fills a.tiles_* for the large kernel.
+hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratch sk = {}, int cus = 0,
+                          const ddg::AdapterArgs* ad = nullptr) {
   if (a.m <= 16) {
     // Wide outputs (at least 200 workgroups of 64 columns): the
     // weight-streaming kernel with an 8-way K split and X in registers.  Below
@@ -255,7 +269,7 @@ hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratc
       while (lds() > ddg::kLdsLimit && (ncb > 1 || kc > 3)) {
         if (ncb > 1) ncb /= 2; else --kc;
       }
-      if (lds() <= ddg::kLdsLimit) return by_bits<SkinnyF>(bits, a, kc, ncb, stream);
+      if (lds() <= ddg::kLdsLimit) return by_bits<SkinnyF>(bits, ad, stream, a, kc, ncb);
     }
   }
   if (a.m <= 16 && sk.p != nullptr && cus > 0) {
@@ -270,7 +284,7 @@ hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratc
                                                        align256((size_t)nb4 * ddg::kSmallMaxParts * 1024));
       sp.epoch = next_epoch();
       sp.parts = parts;
-      return by_bits<SmallSplitF>(bits, a, kSplitNc, sp, stream);
+      return by_bits<SmallSplitF>(bits, ad, stream, a, kSplitNc, sp);
     }
   }
   if (a.m <= 64) {
@@ -288,7 +302,7 @@ hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratc
     } else if (nb / 2 >= 128) {
       nc = 2; nk = rb == 1 ? 4 : 2;
     }
-    return by_bits<SmallF>(bits, a, rb, nc, nk, stream);
+    return by_bits<SmallF>(bits, ad, stream, a, rb, nc, nk);
   }
   // large kernel: 256 x 256 tiles
   a.tiles_m = (a.m + ddg::kBM - 1) / ddg::kBM;
@@ -301,7 +315,7 @@ hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratc
     const int tn192 = (int)((a.n + ddg::kBN192 - 1) / ddg::kBN192);
     if (prefer_n192(tiles, (int64_t)a.tiles_m * tn192, form, cus)) {
       a.tiles_n = tn192;
-      return by_bits<N192F>(bits, a, stream);
+      return by_bits<N192F>(bits, ad, stream, a);
     }
   }
   if (form != 0 && sk.bytes >= (size_t)grid_max * kSkSlotBytes + (size_t)grid_max * sizeof(unsigned long long)) {
@@ -312,9 +326,9 @@ hipError_t launch_product(ddg::GemmArgs& a, int bits, hipStream_t stream, Scratc
     k.wpx = grid_max / ddg::kSkXcds;
     k.split = form > 0 ? form : 0;
     const int grid = form > 0 ? form * (int)tiles : grid_max;
-    return by_bits<StreamKF>(bits, a, k, grid, stream);
+    return by_bits<StreamKF>(bits, ad, stream, a, k, grid);
   }
-  return by_bits<LargeF>(bits, a, stream);
+  return by_bits<LargeF>(bits, ad, stream, a);
 }
 
 // Bytes of the low-rank intermediate T (M x r bf16), rounded up to 256.
@@ -326,6 +340,25 @@ size_t lowrank_part_bytes(int64_t m, int64_t k, int r) {
   if (m <= 0 || m > 64 || k / DDG_GROUP < 8 || r <= 0) return 0;
   int gpc = 1;
   const int chunks = ddg::lowrank_split_chunks((int)k, &gpc);
+  return align256((size_t)chunks * (size_t)m * (size_t)r * 4);
+}
+
+// K chunks of the adapters' pre-pass for m rows at rank r (gpc groups of 128
+// per chunk): enough workgroups for two per compute unit, at most
+// kAdapterMaxChunks partial sums for the product to add.
+int adapter_chunks(int64_t m, int64_t k, int r, int* gpc) {
+  const int64_t g = k / DDG_GROUP;
+  const int64_t blocks = (m + 15) / 16;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ddg::kAdapterMaxChunks, 512 / std::max<int64_t>(blocks, 1)));
+  *gpc = (int)((g + want - 1) / want);
+  return (int)((g + *gpc - 1) / *gpc);
+}
+
+// Bytes of the adapters' T (chunks x M x r float32), rounded up to 256.
+size_t adapter_t_bytes(int64_t m, int64_t k, int r) {
+  if (m <= 0 || k < DDG_GROUP) return 0;
+  int gpc = 1;
+  const int chunks = adapter_chunks(m, k, r, &gpc);
   return align256((size_t)chunks * (size_t)m * (size_t)r * 4);
 }
 
@@ -613,6 +646,61 @@ int ddg_lowrank_fused_gemm(const void* x, int64_t m, int64_t k, const uint8_t* p
   }
   return hip_status(launch_lowrank(x, m, k, packed, scales, bits, n, lora_down, lora_up, r, y, y_dtype,
                                    static_cast<__bf16*>(workspace), stream, sk, cus));
+}
+
+int ddg_adapter_workspace_bytes(int64_t m, int64_t n, int64_t k, int r, int split, size_t* bytes) {
+  if (!bytes) return DDG_ERR_ARG;
+  if (m < 0 || m > kLowrankMaxM || n < 0 || n > kMaxDim || !k_ok(k) || k > kMaxK || r < 8 || r > 128 || r % 8)
+    return DDG_ERR_SHAPE;
+  *bytes = adapter_t_bytes(m, k, r) + (split ? std::max(streamk_bytes(m, n), small_split_bytes(m, n, k)) : 0);
+  return DDG_OK;
+}
+
+int ddg_adapter_gemm(const void* x, int64_t m, int64_t k, const uint8_t* packed, const float* scales, int bits,
+                     int64_t n, const void* down, const void* up, const float* adapter_scales, int64_t adapters,
+                     int r, const int32_t* rows, void* y, int y_dtype, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream) {
+  if (int st = check_gemm(x, m, k, packed, scales, bits, n, y, y_dtype)) return st;
+  if (r < 8 || r > 128 || r % 8 || m > kLowrankMaxM || adapters < 1 || adapters > kMaxDim ||
+      !mul_ok(adapters, std::max(n, k) * r))
+    return DDG_ERR_SHAPE;
+  if (m == 0) return DDG_OK;
+  if (!down || !up || !adapter_scales || !rows || !workspace) return DDG_ERR_ARG;
+  if (!aligned(down, 16) || !aligned(up, 16) || !aligned(adapter_scales, 4) || !aligned(rows, 4) ||
+      !aligned(workspace, 16))
+    return DDG_ERR_ALIGN;
+  const size_t t_bytes = adapter_t_bytes(m, k, r);
+  if (workspace_bytes < t_bytes) return DDG_ERR_WORKSPACE;
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  Scratch sk;
+  if (workspace_bytes > t_bytes) {
+    sk.p = static_cast<uint8_t*>(workspace) + t_bytes;
+    sk.bytes = workspace_bytes - t_bytes;
+  }
+  ddg::AdapterDown d{};
+  d.x = static_cast<const __bf16*>(x);
+  d.down = static_cast<const __bf16*>(down);
+  d.scales = adapter_scales;
+  d.rows = rows;
+  d.t = static_cast<float*>(workspace);
+  d.m = (int)m; d.k = (int)k; d.r = r; d.count = (int)adapters;
+  d.chunks = adapter_chunks(m, k, r, &d.gpc);
+  if (hipError_t e = ddg::launch_adapter_down(d, stream)) return hip_status(e);
+  ddg::AdapterArgs ad{};
+  ad.rows = rows;
+  ad.t = d.t;
+  ad.up = static_cast<const __bf16*>(up);
+  ad.count = d.count;
+  ad.chunks = d.chunks;
+  ddg::GemmArgs a{};
+  a.x = d.x;
+  a.packed = packed;
+  a.scales = scales;
+  a.y = y;
+  a.m = (int)m; a.n = (int)n; a.k = (int)k; a.r = r;
+  a.out_bf16 = y_dtype == DDG_BF16;
+  return hip_status(launch_product(a, bits, stream, sk, cus, &ad));
 }
 
 }  // extern "C"

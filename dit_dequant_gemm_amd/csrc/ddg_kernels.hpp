@@ -19,6 +19,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "ddg_adapters.hpp"
 #include "ddg_device.hpp"
 
 namespace ddg {
@@ -247,9 +248,11 @@ __device__ __forceinline__ f32x16 mfma32x32x16(bf16x8 a, bf16x8 b, f32x16 c) {
 // T * lora_up^T of the tile is added first.  `lds` is the workgroup's 128 KB
 // LDS block; on return the last group's LDS reads may still be pending in
 // other waves (a barrier must precede any reuse of LDS).
-template <int B>
+// Ad = AdapterArgs: the rows' adapters instead.
+template <int B, typename Ad = NoAdapters>
 __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, int tn, int g0, int g1,
-                                                 bool lowrank, f32x16 (&acc)[kBM / 32], uint8_t* lds) {
+                                                 bool lowrank, f32x16 (&acc)[kBM / 32], uint8_t* lds,
+                                                 const Ad& ad = Ad{}) {
   constexpr int RB = kBM / 32;          // 8 row blocks of 32
   constexpr int LA = 4;                 // A-operand look-ahead, in MFMA steps
   constexpr int RING = 8;               // A-operand ring (64 steps per group = 8 laps)
@@ -342,7 +345,10 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
   // the low-rank branch's loads go out behind the first group's, so that
   // their latencies overlap (32760 x 5120 x 5120, r = 32: 1558 -> 1504 us for
   // the fused call); it still adds into acc before the K loop
-  if (lowrank && args.t != nullptr) {
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    if (lowrank)
+      adapter_tile32(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, m0, min(nw0 + wave * 32 + lr, args.n - 1), acc);
+  } else if (lowrank && args.t != nullptr) {
     // acc = T * lora_up^T over the rank dimension, 16 at a time (zero-padded).
     const int R = args.r;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
@@ -452,13 +458,13 @@ __device__ __forceinline__ void zero_acc(f32x16 (&acc)[kBM / 32]) {
 // One whole 256 x 256 output tile (tile index `tile`).  Kernels:
 // gemm_large_kernel (one product) and gemm_grouped_large_kernel (several
 // products in one launch).
-template <int B>
-__device__ __forceinline__ void large_tile(const GemmArgs& args, int tile, uint8_t* lds) {
+template <int B, typename Ad = NoAdapters>
+__device__ __forceinline__ void large_tile(const GemmArgs& args, int tile, uint8_t* lds, const Ad& ad = Ad{}) {
   int tm, tn;
   tile_coords(tile, args.tiles_m, args.tiles_n, tm, tn);
   f32x16 acc[kBM / 32];
   zero_acc(acc);
-  large_accumulate<B>(args, tm, tn, 0, args.k / kGroup, true, acc, lds);
+  large_accumulate<B>(args, tm, tn, 0, args.k / kGroup, true, acc, lds, ad);
   __syncthreads();
   large_store(args, tm, tn, acc, lds);
 }
@@ -467,6 +473,12 @@ template <int B>
 __global__ __launch_bounds__(512, 1) void gemm_large_kernel(GemmArgs args) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kLdsStage];
   large_tile<B>(args, blockIdx.x, lds);
+}
+
+template <int B>
+__global__ __launch_bounds__(512, 1) void gemm_large_adapter_kernel(GemmArgs args, AdapterArgs ad) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kLdsStage];
+  large_tile<B>(args, blockIdx.x, lds, ad);
 }
 
 // ---------------------------------------------------------------------------
@@ -489,8 +501,8 @@ __global__ __launch_bounds__(512, 1) void gemm_large_kernel(GemmArgs args) {
 constexpr int kBN192 = 192;
 constexpr int kEpi48Stride = 52;     // floats per scratch row (48 + 4: conflict-free writes)
 
-template <int B>
-__device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, uint8_t* lds) {
+template <int B, typename Ad = NoAdapters>
+__device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, uint8_t* lds, const Ad& ad = Ad{}) {
   constexpr int RB = kBM / 16;          // 16 row blocks of 16
   constexpr int CB = 3;                 // column blocks of 16 per wave
   constexpr int KS = 4;                 // k-steps of 32 per group
@@ -601,7 +613,12 @@ __device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, 
   load_w(0, wn, sn);
   // the low-rank branch behind the first group's loads, as in K2
   // (4096 x 3072 x 3072, r = 32: 87.6 -> 84.3 us for the fused call)
-  if (args.t != nullptr) {
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    int n[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) n[c] = min(nw0 + (int)ncol + 16 * c, args.n - 1);
+    adapter_tile16(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, m0, n, acc);
+  } else if (args.t != nullptr) {
     // acc = T * lora_up^T over the rank dimension, 32 at a time (zero-padded).
     const int R = args.r;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
@@ -789,6 +806,14 @@ __global__ __launch_bounds__(256, 1) void gemm_n192_kernel(GemmArgs args) {
   n192_tile<B>(args, tm, tn, lds);
 }
 
+template <int B>
+__global__ __launch_bounds__(256, 1) void gemm_n192_adapter_kernel(GemmArgs args, AdapterArgs ad) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kLdsStage];
+  int tm, tn;
+  tile_coords<2>(blockIdx.x, args.tiles_m, args.tiles_n, tm, tn);
+  n192_tile<B>(args, tm, tn, lds, ad);
+}
+
 // ---------------------------------------------------------------------------
 // K2sk: the large-M product with K split across workgroups, for outputs whose
 // 256 x 256 tiles would fill the compute units unevenly.  At most one
@@ -842,8 +867,9 @@ constexpr unsigned kSkSpinLimit = 1u << 20;
 constexpr int kSkCoherent = 16;   // SC1
 constexpr int kSkMaxSplit = 8;    // K chunks per tile in split-K
 
-template <int B>
-__global__ __launch_bounds__(512, 1) void gemm_streamk_kernel(GemmArgs args, StreamK sk) {
+// (Ad: nothing, or AdapterArgs)
+template <int B, typename... Ad>
+__global__ __launch_bounds__(512, 1) void gemm_streamk_kernel(GemmArgs args, StreamK sk, Ad... ad) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kLdsStage];
   const int w = blockIdx.x;
   const int G = args.k / kGroup;
@@ -903,7 +929,7 @@ __global__ __launch_bounds__(512, 1) void gemm_streamk_kernel(GemmArgs args, Str
     }
     f32x16 acc[kBM / 32];
     zero_acc(acc);
-    large_accumulate<B>(args, tm, tn, a, b, a == 0, acc, lds);
+    large_accumulate<B>(args, tm, tn, a, b, a == 0, acc, lds, ad...);
     __syncthreads();
     if (split_k) {
       // every chunk publishes its partial tile, then reduces and stores the
@@ -1085,10 +1111,10 @@ struct SmallSplit {
 };
 constexpr int kSmallMaxParts = 8;
 
-template <int B, int RB, int NC, int NK>
+template <int B, int RB, int NC, int NK, typename Ad = NoAdapters>
 __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLds<RB, NC, NK>& L,
                                            const SmallSplit& sp = SmallSplit{nullptr, nullptr, 0, 1},
-                                           int part = 0) {
+                                           int part = 0, const Ad& ad = Ad{}) {
   // X slices and packed weights of step j + D are loaded into registers at
   // step j (rings of S = D + 1 slots); at step j each wave writes its share of
   // X(j) to the LDS slot, and one LDS barrier hands the slot to the other
@@ -1233,6 +1259,19 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
     for (int i = 0; i < 4; ++i)
       acc[rb][i] = (acc4[0][rb][i] + acc4[1][rb][i]) + (acc4[2][rb][i] + acc4[3][rb][i]);
 
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    // the K splits share out the distinct adapters
+    const int nn[1] = {n};
+    f32x4 br[RB][1];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) br[rb][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    adapter_rows16<RB, 1>(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, nn, part * NK + h, sp.parts * NK, br);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[rb][i] += br[rb][0][i];
+  }
+
   if constexpr (NK > 1) {
     if (h > 0) {
 #pragma unroll
@@ -1291,7 +1330,7 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
     }
   }
 
-  if (args.t != nullptr) {
+  if (!std::is_same_v<Ad, AdapterArgs> && args.t != nullptr) {
     const int R_ = args.r;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
     for (int j0 = 0; j0 < R_; j0 += 32) {
@@ -1324,12 +1363,26 @@ __global__ __launch_bounds__(64 * NC * NK) void gemm_small_kernel(GemmArgs args)
   small_body<B, RB, NC, NK>(args, blockIdx.x, L);
 }
 
+template <int B, int RB, int NC, int NK>
+__global__ __launch_bounds__(64 * NC * NK) void gemm_small_adapter_kernel(GemmArgs args, AdapterArgs ad) {
+  __shared__ SmallLds<RB, NC, NK> L;
+  small_body<B, RB, NC, NK>(args, blockIdx.x, L, SmallSplit{nullptr, nullptr, 0, 1}, 0, ad);
+}
+
 // M <= 16 with K split across workgroups: workgroup id = wg * parts + part.
 template <int B, int NC>
 __global__ __launch_bounds__(64 * NC) void gemm_small_split_kernel(GemmArgs args, SmallSplit sp) {
   __shared__ SmallLds<1, NC, 1> L;
   const int wg = blockIdx.x / sp.parts, part = blockIdx.x - wg * sp.parts;
   small_body<B, 1, NC, 1>(args, wg, L, sp, part);
+}
+
+template <int B, int NC>
+__global__ __launch_bounds__(64 * NC) void gemm_small_split_adapter_kernel(GemmArgs args, SmallSplit sp,
+                                                                           AdapterArgs ad) {
+  __shared__ SmallLds<1, NC, 1> L;
+  const int wg = blockIdx.x / sp.parts, part = blockIdx.x - wg * sp.parts;
+  small_body<B, 1, NC, 1>(args, wg, L, sp, part, ad);
 }
 
 // ---------------------------------------------------------------------------
@@ -1381,9 +1434,9 @@ struct SkinnyLds {
 // Workgroup wg of the product `args` (see the comment above).  wl0, wl1 and
 // scw are LDS arrays of at least SkinnyLds<B, KC, NCB>::W0, ::W1 bytes and
 // [8][KC][64] floats.
-template <int B, int KC, int NCB>
+template <int B, int KC, int NCB, typename Ad = NoAdapters>
 __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_t* wl0, uint8_t* wl1,
-                                            float (*scw)[KC][64]) {
+                                            float (*scw)[KC][64], const Ad& ad = Ad{}) {
   constexpr int NW = SkinnyLds<B, KC, NCB>::NW;       // waves = K splits
   constexpr uint32_t kNoLoad = 0x80000000u;
   constexpr int NDMA = SkinnyLds<B, KC, NCB>::NDMA;
@@ -1527,6 +1580,22 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
     }(std::make_integer_sequence<int, CU>{});
   }
 
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    // the eight K splits share out the distinct adapters
+    int n[NCB];
+    f32x4 br[1][NCB];
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) {
+      n[cb] = min(n0 + cb * 16 + lr, args.n - 1);
+      br[0][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    adapter_rows16<1, NCB>(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, n, wave, NW, br);
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[cb][0][i] += br[0][cb][i];
+  }
+
   // sum the 8 partial tiles of each column block; wave cb finishes block cb
   // (the reduction reuses the first weight buffer: every DMA must have landed)
   __builtin_amdgcn_s_waitcnt(0);
@@ -1548,7 +1617,7 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
     tot[0] += v[0]; tot[1] += v[1]; tot[2] += v[2]; tot[3] += v[3];
   }
   const int n = min(n0 + cb * 16 + lr, args.n - 1);
-  if (args.t != nullptr) {
+  if (!std::is_same_v<Ad, AdapterArgs> && args.t != nullptr) {
     const int R_ = args.r;
     const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
     for (int j0 = 0; j0 < R_; j0 += 32) {
@@ -1574,6 +1643,15 @@ __global__ __launch_bounds__(512) void gemm_skinny_kernel(GemmArgs args) {
   __shared__ __attribute__((aligned(1024))) uint8_t wl1[L::W1];
   __shared__ __attribute__((aligned(256))) float scw[L::NW][KC][64];
   skinny_body<B, KC, NCB>(args, blockIdx.x, wl0, wl1, scw);
+}
+
+template <int B, int KC, int NCB>
+__global__ __launch_bounds__(512) void gemm_skinny_adapter_kernel(GemmArgs args, AdapterArgs ad) {
+  using L = SkinnyLds<B, KC, NCB>;
+  __shared__ __attribute__((aligned(1024))) uint8_t wl0[L::W0];
+  __shared__ __attribute__((aligned(1024))) uint8_t wl1[L::W1];
+  __shared__ __attribute__((aligned(256))) float scw[L::NW][KC][64];
+  skinny_body<B, KC, NCB>(args, blockIdx.x, wl0, wl1, scw, ad);
 }
 
 // ---------------------------------------------------------------------------

@@ -61,6 +61,35 @@ hipError_t launch_rpbh_rotate(const void* x, bool f32_in, int64_t n, int d, cons
                               const int8_t* signs, int h, void* out, bool f32_out, int cus,
                               hipStream_t stream);
 
+// The products above with an adapter per row, and the pre-pass that writes
+// ad.t (chunks x m x r float32; chunk c: gpc groups of 128 inputs).
+template <int B>
+hipError_t launch_adapter_large(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream);
+template <int B>
+hipError_t launch_adapter_n192(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream);
+template <int B>
+hipError_t launch_adapter_streamk(const GemmArgs& a, const StreamK& sk, int grid, const AdapterArgs& ad,
+                                  hipStream_t stream);
+// (1,8) (2,4) (4,2) for rb = 1, (1,4) (2,2) otherwise
+template <int B>
+hipError_t launch_adapter_small(const GemmArgs& a, int rb, int nc, int nk, const AdapterArgs& ad, hipStream_t stream);
+template <int B>
+hipError_t launch_adapter_small_split(const GemmArgs& a, int nc, const SmallSplit& sp, const AdapterArgs& ad,
+                                      hipStream_t stream);
+template <int B>
+hipError_t launch_adapter_skinny(const GemmArgs& a, int kc, int ncb, const AdapterArgs& ad, hipStream_t stream);
+struct AdapterDown {
+  const __bf16* x;          // m x k
+  const __bf16* down;       // count x r x k
+  const float* scales;      // count
+  const int* rows;          // m
+  float* t;
+  int m, k, r, count, chunks, gpc;
+};
+hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream);
+// Row blocks of 16 per workgroup of a pre-pass for m rows at rank r.
+int lowrank_t_row_blocks(int m, int r);
+
 // Rotary positions of q (and, with k.heads > 0, k), behind a norm or alone.
 // Strides in elements; w: norm weights (head: dim values, token: heads x dim)
 // or null; ends: prefix sums of the axes' pair counts (INT_MAX from the last

@@ -282,6 +282,49 @@ int ddg_lowrank_fused_gemm_noalloc(const void* x, int64_t m, int64_t k, const ui
                                    void* y, int y_dtype, hipStream_t stream);
 
 /*
+ * The product with low-rank adapters of many requests at once: the rows of X
+ * come from several requests that share the quantized weight, each with an
+ * adapter of its own (or none),
+ *   Y[i] = X[i] * w_hat^T + s_a (X[i] * D_a^T) * U_a^T,  a = rows[i],
+ * D_a and U_a in the layout of linear weights (out x in):
+ *   down            adapters x r x K bf16 (D_a: the a-th r x K)
+ *   up              adapters x N x r bf16
+ *   adapter_scales  adapters float32 (s_a, e.g. alpha / rank)
+ *   rows            M int32; a value outside [0, adapters) means no adapter
+ * Adapters of smaller rank are padded with zero rows of D and columns of U.
+ * Any order of rows is allowed; runs of equal values are the fast case (a
+ * block of 16 to 32 rows does each of its distinct adapters' work).  Neither
+ * factor of an adapter that no row names is read, and an adapter's infinities
+ * and NaNs reach only the rows that name it.
+ * T = s_a X[i] D_a^T is summed in float32 and enters the matrix product in
+ * bf16 parts that hold it to 2^-16 for a bf16 y and to 2^-24 for a float32 y;
+ * the branch is summed into the product's float32 accumulator, rounded once.
+ *   workspace  device scratch: T in float32 first (required:
+ *              ddg_adapter_workspace_bytes with split = 0), then optionally
+ *              the split-K area of ddg_dequant_gemm (split = 1).  Its contents
+ *              are scratch.  Calls that share it must be ordered.  Under graph
+ *              capture, pass the first part alone (see ddg_dequant_gemm).
+ * Requirements: as ddg_dequant_gemm, plus 8 <= r <= 128, r % 8 == 0, M at most
+ * 2^28 - 16, adapters in 1 .. 2^31 - 1; down, up and workspace 16-byte aligned.
+ * Errors: DDG_ERR_ARG, DDG_ERR_SHAPE, DDG_ERR_ALIGN, DDG_ERR_WORKSPACE,
+ * DDG_ERR_HIP, DDG_ERR_UNSUPPORTED.
+ */
+int ddg_adapter_gemm(const void* x, int64_t m, int64_t k, const uint8_t* packed, const float* scales, int bits,
+                     int64_t n, const void* down, const void* up, const float* adapter_scales, int64_t adapters,
+                     int r, const int32_t* rows, void* y, int y_dtype, void* workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+
+/*
+ * Workspace bytes of ddg_adapter_gemm: T (M x r float32 for each of at most 8
+ * parts of K that the pre-pass spreads over workgroups, rounded up to 256)
+ * and, with split != 0, the split-K area of ddg_dequant_gemm.  Host-only.
+ * Errors: DDG_ERR_ARG (null), DDG_ERR_SHAPE (m negative or above 2^28 - 16, n
+ * negative or above 2^31 - 1, k not a positive multiple of 128 up to 2^20, r
+ * outside 8..128 or not a multiple of 8).
+ */
+int ddg_adapter_workspace_bytes(int64_t m, int64_t n, int64_t k, int r, int split, size_t* bytes);
+
+/*
  * Quantization error of an N x K weight at every width 3..7 ([WDQ] §3.2:
  * the per-tensor error tables the bit allocation searches over; §3.1: the
  * quantizer of ddg_quantize_pack, float32 arithmetic bit for bit):
