@@ -1,5 +1,7 @@
 // The products with per-row adapters for one bit width, DDG_BITS, and (in the
 // unit of width 4) the launcher of their pre-pass.  Compiled once per width.
+#include <algorithm>
+
 #include "ddg_launch.hpp"
 
 #ifndef DDG_BITS
@@ -71,39 +73,40 @@ hipError_t launch_adapter_skinny<DDG_BITS>(const GemmArgs& a, int kc, int ncb, c
 
 #if DDG_BITS == 4
 namespace {
-template <int RBLK, int RR>
-hipError_t launch_rr(const AdapterDown& d, int z, hipStream_t stream) {
+template <int RBLK, int RR, int NW, bool PARTS>
+hipError_t launch_down(const AdapterDown& d, int z, hipStream_t stream) {
   const dim3 grid((unsigned)((d.m + 16 * RR - 1) / (16 * RR)), (unsigned)d.chunks, (unsigned)z);
-  adapter_down_kernel<RBLK, RR><<<grid, dim3(64 * kAdapterWaves), 0, stream>>>(d.x, d.down, d.scales, d.rows, d.count,
-                                                                             d.t, d.m, d.k, d.r, d.gpc);
+  adapter_down_kernel<RBLK, RR, NW, PARTS><<<grid, dim3(64 * NW), 0, stream>>>(d);
   return hipGetLastError();
 }
 
 template <int RBLK>
-hipError_t launch_rblk(const AdapterDown& d, int rr, int z, hipStream_t stream) {
+hipError_t launch_rblk(const AdapterDown& d, hipStream_t stream) {
+  // at most 64 rows: every distinct adapter of a row block in a workgroup of its own
+  if (d.m <= kAdapterFewRows) return launch_down<RBLK, 1, 16, false>(d, std::min(d.count, 16), stream);
+  // a block's second adapter goes to a second workgroup: blocks with a
+  // request's end inside would otherwise take twice as long as the others
+  const int rr = lowrank_t_row_blocks(d.m, d.r);
   if constexpr (RBLK <= 2) {
-    if (rr == 4) return launch_rr<RBLK, 4>(d, z, stream);
+    if (rr == 4) return launch_down<RBLK, 4, 8, true>(d, std::min(d.count, 2), stream);
   }
   if constexpr (RBLK <= 4) {
-    if (rr == 2) return launch_rr<RBLK, 2>(d, z, stream);
+    if (rr == 2) return launch_down<RBLK, 2, 8, true>(d, std::min(d.count, 2), stream);
   }
-  return launch_rr<RBLK, 1>(d, z, stream);
+  return launch_down<RBLK, 1, 16, true>(d, std::min(d.count, 2), stream);
 }
 }  // namespace
 
 hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream) {
-  const int rr = lowrank_t_row_blocks(d.m, d.r);
-  // few rows: the distinct adapters of a row block go to four workgroups
-  const int z = d.m <= 64 ? 4 : 1;
   switch ((d.r + 15) / 16) {
-    case 1: return launch_rblk<1>(d, rr, z, stream);
-    case 2: return launch_rblk<2>(d, rr, z, stream);
-    case 3: return launch_rblk<3>(d, rr, z, stream);
-    case 4: return launch_rblk<4>(d, rr, z, stream);
-    case 5: return launch_rblk<5>(d, rr, z, stream);
-    case 6: return launch_rblk<6>(d, rr, z, stream);
-    case 7: return launch_rblk<7>(d, rr, z, stream);
-    case 8: return launch_rblk<8>(d, rr, z, stream);
+    case 1: return launch_rblk<1>(d, stream);
+    case 2: return launch_rblk<2>(d, stream);
+    case 3: return launch_rblk<3>(d, stream);
+    case 4: return launch_rblk<4>(d, stream);
+    case 5: return launch_rblk<5>(d, stream);
+    case 6: return launch_rblk<6>(d, stream);
+    case 7: return launch_rblk<7>(d, stream);
+    case 8: return launch_rblk<8>(d, stream);
     default: return hipErrorInvalidValue;
   }
 }

@@ -343,23 +343,24 @@ size_t lowrank_part_bytes(int64_t m, int64_t k, int r) {
   return align256((size_t)chunks * (size_t)m * (size_t)r * 4);
 }
 
-// K chunks of the adapters' pre-pass for m rows at rank r (gpc groups of 128
-// per chunk): enough workgroups for two per compute unit, at most
-// kAdapterMaxChunks partial sums for the product to add.
-int adapter_chunks(int64_t m, int64_t k, int r, int* gpc) {
+// K chunks of the adapters' pre-pass for at most kAdapterFewRows rows (gpc
+// groups of 128 per chunk): about four steps of 32 inputs for each of a
+// workgroup's 16 waves, at most kAdapterMaxChunks sums for the product to add.
+// More rows: one chunk.
+int adapter_chunks(int64_t m, int64_t k, int* gpc) {
   const int64_t g = k / DDG_GROUP;
-  const int64_t blocks = (m + 15) / 16;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ddg::kAdapterMaxChunks, 512 / std::max<int64_t>(blocks, 1)));
+  const int64_t want = m <= ddg::kAdapterFewRows ? std::min<int64_t>(ddg::kAdapterMaxChunks, (g + 15) / 16) : 1;
   *gpc = (int)((g + want - 1) / want);
   return (int)((g + *gpc - 1) / *gpc);
 }
 
-// Bytes of the adapters' T (chunks x M x r float32), rounded up to 256.
+// Bytes of the adapters' T, rounded up to 256: chunks x M x r float32, or
+// kAdapterMaxParts x M x r bf16.
 size_t adapter_t_bytes(int64_t m, int64_t k, int r) {
-  if (m <= 0 || k < DDG_GROUP) return 0;
+  if (m <= 0) return 0;
   int gpc = 1;
-  const int chunks = adapter_chunks(m, k, r, &gpc);
-  return align256((size_t)chunks * (size_t)m * (size_t)r * 4);
+  const size_t per = m <= ddg::kAdapterFewRows ? (size_t)adapter_chunks(m, k, &gpc) * 4 : (size_t)ddg::kAdapterMaxParts * 2;
+  return align256(per * (size_t)m * (size_t)r);
 }
 
 // T = bf16(X L1) into t, then the product with the branch in its epilogue.
@@ -683,16 +684,20 @@ int ddg_adapter_gemm(const void* x, int64_t m, int64_t k, const uint8_t* packed,
   d.down = static_cast<const __bf16*>(down);
   d.scales = adapter_scales;
   d.rows = rows;
-  d.t = static_cast<float*>(workspace);
+  d.part = static_cast<float*>(workspace);
+  d.t16 = static_cast<__bf16*>(workspace);
   d.m = (int)m; d.k = (int)k; d.r = r; d.count = (int)adapters;
-  d.chunks = adapter_chunks(m, k, r, &d.gpc);
+  d.chunks = adapter_chunks(m, k, &d.gpc);
+  d.parts = y_dtype == DDG_BF16 ? 2 : 3;
   if (hipError_t e = ddg::launch_adapter_down(d, stream)) return hip_status(e);
   ddg::AdapterArgs ad{};
   ad.rows = rows;
-  ad.t = d.t;
+  ad.t = d.part;
+  ad.t16 = d.t16;
   ad.up = static_cast<const __bf16*>(up);
   ad.count = d.count;
   ad.chunks = d.chunks;
+  ad.parts = d.parts;
   ddg::GemmArgs a{};
   a.x = d.x;
   a.packed = packed;

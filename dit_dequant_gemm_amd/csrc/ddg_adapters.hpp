@@ -1,24 +1,27 @@
 // Low-rank adapters of many requests beside one shared product: row i of Y
 // also gets s_a T_i U_a^T with a = rows[i] and T_i = X_i D_a^T.
 //
-//   adapter_down_kernel  T (times s_a) in float32, K in `chunks` parts whose
-//                        sums the product adds up, in order;
-//   adapter_tile32 / adapter_tile16 / adapter_rows16
-//                        the branch inside the product kernels: the first
-//                        terms of their accumulators.
+//   adapter_down_kernel   T (times s_a): for at most 64 rows float32 sums over
+//                         `chunks` parts of K, which the product adds up in
+//                         order; for more rows the bf16 parts of T
+//   adapter_tile          the branch of a 256-row tile
+//   adapter_stage, adapter_first, adapter_rows16
+//                         the branch of at most 64 rows
 //
 // A block of rows may mix adapters.  Every wave walks the distinct adapters of
 // its rows (ballots over the ids held one row per lane, so the walk is uniform
-// over the wave) and runs the matrix instructions of one adapter for the row
-// blocks that hold it, with the other rows' T as zeros.  Requests are runs of
-// rows, so most blocks hold one adapter and cost what one shared adapter does.
-// A block that mixes adapters adds each adapter's sums to that adapter's rows
-// only: an infinity or NaN among its weights reaches no other request.
+// over the wave) and runs the matrix instructions of one adapter at a time,
+// the other rows' T as zeros.  Requests are runs of rows, so most blocks hold
+// one adapter and cost what one shared adapter does.  An infinity or NaN in
+// an adapter's U times another row's zero would be a NaN: mixed tiles take it
+// out of the operand and make the outputs of the adapter's own rows infinite,
+// mixed blocks of few rows keep an adapter's sums apart and add them to its
+// own rows only.
 //
-// T is float32 and enters the bf16 matrix instructions as a sum of bf16
-// parts: two (to 2^-16 of T) for a bf16 Y, whose own
-// rounding is 2^-8, and three (to 2^-24) for a float32 Y.  The products of
-// bf16 parts are exact in the float32 accumulator, so Y is rounded once.
+// T enters the bf16 matrix instructions as a sum of bf16 parts: two (to 2^-16
+// of T) for a bf16 Y, whose own rounding is 2^-8, and three (to 2^-24) for a
+// float32 Y.  The products of bf16 values are exact in the float32
+// accumulator, so Y is rounded once.
 #pragma once
 
 #include "ddg_device.hpp"
@@ -27,44 +30,26 @@ namespace ddg {
 
 struct AdapterArgs {
   const int* rows;          // M adapter numbers; outside [0, count): no adapter
-  const float* t;           // chunks x M x R
+  const float* t;           // at most 64 rows: chunks x M x R
+  const __bf16* t16;        // more rows: parts x M x R
   const __bf16* up;         // count x N x R
   int count;
   int chunks;
+  int parts;
 };
 struct NoAdapters {};       // a product without them
 
 constexpr int kAdapterMaxChunks = 8;
+constexpr int kAdapterMaxParts = 3;
 
 // Row r's adapter, -1 for none and for rows past m.
 __device__ __forceinline__ int adapter_of(const int* rows, int count, int r, int m) {
-  const int id = r < m ? rows[r] : -1;
-  return (unsigned)id < (unsigned)count ? id : -1;
-}
-
-// Eight values of T_row from column kc on, its chunks added in order.
-__device__ __forceinline__ void adapter_t8(const AdapterArgs& ad, int row, int m, int R, int kc, float (&t)[8]) {
-  const float* p = ad.t + (int64_t)row * R + kc;
-  const int64_t chunk = (int64_t)m * R;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    t[i] = a[i];
-    t[4 + i] = b[i];
-  }
-  for (int c = 1; c < ad.chunks; ++c) {
-    const f32x4 u = *reinterpret_cast<const f32x4*>(p + c * chunk);
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p + c * chunk + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      t[i] += u[i];
-      t[4 + i] += v[i];
-    }
-  }
+  const int id = rows[min(r, m - 1)];
+  return r < m && (unsigned)id < (unsigned)count ? id : -1;
 }
 
 // The next bf16 part of t (nearest), which is taken off t.
-__device__ __forceinline__ bf16x8 take_part(float (&t)[8]) {
+__device__ __forceinline__ u32x4 take_part(float (&t)[8]) {
   u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -72,7 +57,20 @@ __device__ __forceinline__ bf16x8 take_part(float (&t)[8]) {
     t[2 * i] -= bf16_bits_to_f32(w[i] & 0xFFFFu);
     t[2 * i + 1] -= __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
   }
-  return __builtin_bit_cast(bf16x8, w);
+  return w;
+}
+
+__device__ __forceinline__ bf16x8 keep_or_zero(bf16x8 v, bool keep) {
+  return __builtin_bit_cast(bf16x8, keep ? __builtin_bit_cast(u32x4, v) : u32x4{0u, 0u, 0u, 0u});
+}
+
+// Any infinity or NaN among the lane's values.
+__device__ __forceinline__ bool nonfinite(bf16x8 v) {
+  const u32x4 w = __builtin_bit_cast(u32x4, v);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+  return bad;
 }
 
 __device__ __forceinline__ f32x16 adapter_mfma(bf16x8 a, bf16x8 b, f32x16 c) {
@@ -108,201 +106,273 @@ struct AdapterWalk {
   }
 };
 
-// One k-step of one adapter for a row block whose matching rows are `mask`:
-// lane (row lr, k part q) holds t of its row; b[c] the adapter's columns.
-template <int CB, typename Acc, typename RowOf>
-__device__ __forceinline__ void adapter_block(float (&t)[8], const bf16x8 (&b)[CB], int parts, uint32_t mask,
-                                              uint32_t full, Acc (&acc)[CB], RowOf row_of) {
-  if (mask == full) {
-    for (int p = 0; p < parts; ++p) {
-      const bf16x8 a = take_part(t);
-#pragma unroll
-      for (int c = 0; c < CB; ++c) acc[c] = adapter_mfma(a, b[c], acc[c]);
-    }
-    return;
-  }
-  constexpr int N = sizeof(Acc) / 4;
-  Acc sum[CB];
-#pragma unroll
-  for (int c = 0; c < CB; ++c)
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum[c][i] = 0.0f;
-  for (int p = 0; p < parts; ++p) {
-    const bf16x8 a = take_part(t);
-#pragma unroll
-    for (int c = 0; c < CB; ++c) sum[c] = adapter_mfma(a, b[c], sum[c]);
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const bool mine = (mask >> row_of(i)) & 1;
-#pragma unroll
-    for (int c = 0; c < CB; ++c) acc[c][i] += mine ? sum[c][i] : 0.0f;
-  }
-}
-
-// The branch of a 256-row tile from row m0 for 32 columns (lane column n,
-// clamped to the last), in the 32x32 accumulator layout.
-__device__ __forceinline__ void adapter_tile32(const AdapterArgs& ad, int m, int n_total, int R, int parts, int m0,
-                                               int n, f32x16 (&acc)[8]) {
-  const int lane = threadIdx.x & 63, lr = lane & 31, lh = lane >> 5;
-  const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+// ---------------------------------------------------------------------------
+// 256-row tiles: the branch goes into the accumulators before the K loop.  The
+// tile's first adapter (FIRST) is straight-line code behind the first group's
+// loads, where its latencies overlap theirs.  The other adapters, which only
+// tiles that mix requests have, are a loop ahead of them: a loop over the
+// adapters behind those loads made the compiler spill around the K loop and
+// cost every tile 10 us, also without any adapter (32760 x 15360 x 5120: 4018
+// us for the product alone, 4311 with rows that name none; now 4150 and 4175).
+//
+// T and U are read through buffer resources (one offset register instead of a
+// 64-bit address per row block; rows past M and columns past N read as zeros),
+// and the rows of an adapter are lane masks in scalar registers.
+//
+// ROWS x (256 / ROWS) row blocks, CB column blocks of ROWS from column col0
+// on; lane (row or column l, k part q) of the operands.
+// ---------------------------------------------------------------------------
+template <int ROWS, int CB, bool FIRST, typename Acc>
+__device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n_total, int R, int m0, int col0,
+                                             Acc (&acc)[256 / ROWS][CB]) {
+  constexpr int RB = 256 / ROWS, KS = ROWS == 32 ? 16 : 32;
+  constexpr int BATCH = 8;                                     // T operands in flight
+  const int lane = threadIdx.x & 63, l = lane & (ROWS - 1), q = lane / ROWS;
   int id[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + lane, m);
+  const uint32_t row_bytes = (uint32_t)R * 2;
+  const uint32_t t_bytes = (uint32_t)min(256, m - m0) * row_bytes;
+  const uint32_t u_bytes = (uint32_t)max(0, min(CB * ROWS, n_total - col0)) * row_bytes;
+  const uint32_t lane_off = (uint32_t)l * row_bytes;
   AdapterWalk<4> walk(id);
-  while (walk.next(id)) {
-    const __bf16* up = ad.up + ((int64_t)walk.adapter * n_total + n) * R;
-    uint32_t mask[8];
-#pragma unroll
-    for (int rb = 0; rb < 8; ++rb) mask[rb] = (uint32_t)(walk.match[rb >> 1] >> (32 * (rb & 1)));
-    for (int j0 = 0; j0 < R; j0 += 16) {
-      const int kk = j0 + 8 * lh;
-      const bool kok = kk < R;
-      const int kc = min(kk, R - 8);
-      const bf16x8 v = *reinterpret_cast<const bf16x8*>(up + kc);
-      const bf16x8 b[1] = {kok ? v : zero};
-      // four row blocks' loads in flight at a time (eight spill registers)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float t[4][8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (mask[4 * half + i]) adapter_t8(ad, min(m0 + (4 * half + i) * 32 + lr, m - 1), m, R, kc, t[i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rb = 4 * half + i;
-          if (!mask[rb]) continue;
-          const bool mine = kok && ((mask[rb] >> lr) & 1);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) t[i][e] = mine ? t[i][e] : 0.0f;
-          f32x16 a1[1] = {acc[rb]};
-          adapter_block<1>(t[i], b, parts, mask[rb], 0xFFFFFFFFu, a1,
-                           [&](int e) { return 8 * (e >> 2) + 4 * lh + (e & 3); });
-          acc[rb] = a1[0];
-        }
-      }
-    }
-  }
-}
-
-// The branch of a 256-row tile from row m0 for three blocks of 16 columns
-// (lane columns n[c], clamped to the last), in the 16x16 accumulator layout.
-__device__ __forceinline__ void adapter_tile16(const AdapterArgs& ad, int m, int n_total, int R, int parts, int m0,
-                                               const int (&n)[3], f32x4 (&acc)[16][3]) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-  const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-  int id[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + lane, m);
-  AdapterWalk<4> walk(id);
-  while (walk.next(id)) {
-    const __bf16* up = ad.up + (int64_t)walk.adapter * n_total * R;
-    for (int j0 = 0; j0 < R; j0 += 32) {
-      const int kk = j0 + 8 * lq;
-      const bool kok = kk < R;
-      const int kc = min(kk, R - 8);
-      bf16x8 b[3];
-#pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(up + (int64_t)n[c] * R + kc);
-        b[c] = kok ? v : zero;
-      }
-#pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        float t[4][8];
-        uint32_t mask[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rb = 4 * part + i;
-          mask[i] = (uint32_t)(walk.match[rb >> 2] >> (16 * (rb & 3))) & 0xFFFFu;
-          if (mask[i]) adapter_t8(ad, min(m0 + rb * 16 + lr, m - 1), m, R, kc, t[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!mask[i]) continue;
-          const bool mine = kok && ((mask[i] >> lr) & 1);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) t[i][e] = mine ? t[i][e] : 0.0f;
-          adapter_block<3>(t[i], b, parts, mask[i], 0xFFFFu, acc[4 * part + i], [&](int e) { return 4 * lq + e; });
-        }
-      }
-    }
-  }
-}
-
-// The branch of at most 64 rows for CB blocks of 16 columns (lane columns
-// n[c]); of the distinct adapters, those numbered share, share + shares, ...
-// (the caller's waves split them and add their accumulators up afterwards).
-template <int RB, int CB>
-__device__ __forceinline__ void adapter_rows16(const AdapterArgs& ad, int m, int n_total, int R, int parts,
-                                               const int (&n)[CB], int share, int shares, f32x4 (&acc)[RB][CB]) {
-  const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-  const bf16x8 zero = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-  const int id[1] = {adapter_of(ad.rows, ad.count, lane, m)};
-  AdapterWalk<1> walk(id);
-  for (int d = 0; walk.next(id); d = d + 1 == shares ? 0 : d + 1) {
-    if (d != share) continue;
-    const __bf16* up = ad.up + (int64_t)walk.adapter * n_total * R;
-    for (int j0 = 0; j0 < R; j0 += 32) {
-      const int kk = j0 + 8 * lq;
-      const bool kok = kk < R;
-      const int kc = min(kk, R - 8);
+  if (!walk.next(id)) return;                                  // to the first adapter
+  for (bool more = FIRST || walk.next(id); more; more = !FIRST && walk.next(id)) {
+    const rsrc_t ru = make_rsrc(ad.up + ((int64_t)walk.adapter * n_total + col0) * R, u_bytes);
+    const bool whole = (walk.match[0] & walk.match[1] & walk.match[2] & walk.match[3]) == ~0ull;
+    uint64_t broken[CB] = {};                                  // lanes whose U holds an infinity or a NaN
+    // row block rb's rows of this adapter, for every k part's lanes
+    auto mine = [&](int rb) -> bool {
+      const uint64_t w = walk.match[rb * ROWS / 64] >> (rb * ROWS % 64);
+      return __builtin_amdgcn_inverse_ballot_w64(ROWS == 32 ? (w & 0xFFFFFFFFull) * 0x100000001ull
+                                                            : (w & 0xFFFFull) * 0x1000100010001ull);
+    };
+    for (int j0 = 0; j0 < R; j0 += KS) {
+      const int kk = j0 + 8 * q;
+      // a k part past the rank: past the resource, zeros
+      const uint32_t off = kk < R ? lane_off + (uint32_t)kk * 2 : 0x80000000u;
       bf16x8 b[CB];
 #pragma unroll
       for (int c = 0; c < CB; ++c) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(up + (int64_t)n[c] * R + kc);
-        b[c] = kok ? v : zero;
+        b[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, off + c * ROWS * row_bytes, 0, 0));
+        if (!whole) {
+          const bool bad = nonfinite(b[c]);
+          broken[c] |= __ballot(bad);
+          b[c] = keep_or_zero(b[c], !bad);
+        }
+      }
+      for (int p = 0; p < ad.parts; ++p) {
+        const rsrc_t rt = make_rsrc(ad.t16 + ((int64_t)p * m + m0) * R, t_bytes);
+#pragma unroll
+        for (int r0 = 0; r0 < RB; r0 += BATCH) {
+          bf16x8 a[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i)
+            a[i] = __builtin_bit_cast(
+                bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rt, off + (r0 + i) * ROWS * row_bytes, 0, 0));
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            a[i] = keep_or_zero(a[i], mine(r0 + i));
+#pragma unroll
+            for (int c = 0; c < CB; ++c) acc[r0 + i][c] = adapter_mfma(a[i], b[c], acc[r0 + i][c]);
+          }
+        }
+      }
+    }
+    // its rows' outputs in the columns of an infinity or a NaN: the largest
+    // bf16 squared, an infinity in the accumulator (zeros elsewhere)
+#pragma unroll
+    for (int c = 0; c < CB; ++c) {
+      if (broken[c] == 0) continue;
+      const bf16x8 big = __builtin_bit_cast(bf16x8, u32x4{0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu});
+      bool mark = false;
+#pragma unroll
+      for (int i = 0; i < 64 / ROWS; ++i) mark |= (broken[c] >> (l + i * ROWS)) & 1;
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+        acc[rb][c] = adapter_mfma(keep_or_zero(big, mine(rb)), keep_or_zero(big, mark), acc[rb][c]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// At most 64 rows.  The workgroup adds T's chunks up into LDS once
+// (adapter_stage) as bf16 parts; its K-split waves share out the distinct
+// adapters, and the first two adapters' U of each wave are loaded before the
+// K loop (adapter_first) and used behind it.
+// ---------------------------------------------------------------------------
+constexpr size_t adapter_stage_bytes(int rows) { return (size_t)kAdapterMaxParts * rows * 128 * 2; }
+
+__device__ __forceinline__ void adapter_stage(const AdapterArgs& ad, int m, int R, __bf16* lds, int tid, int n) {
+  const int per_row = R / 8;
+  for (int i = tid; i < m * per_row; i += n) {
+    const float* p = ad.t + (int64_t)i * 8;                   // T is dense: row i / per_row, column 8 (i % per_row)
+    f32x4 lo[kAdapterMaxChunks], hi[kAdapterMaxChunks];
+#pragma unroll
+    for (int c = 0; c < kAdapterMaxChunks; ++c) {
+      // past the last chunk: the last one again, not added
+      const float* pc = p + (int64_t)min(c, ad.chunks - 1) * m * R;
+      lo[c] = *reinterpret_cast<const f32x4*>(pc);
+      hi[c] = *reinterpret_cast<const f32x4*>(pc + 4);
+    }
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t[e] = lo[0][e];
+      t[4 + e] = hi[0][e];
+    }
+#pragma unroll
+    for (int c = 1; c < kAdapterMaxChunks; ++c) {
+      if (c >= ad.chunks) break;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        t[e] += lo[c][e];
+        t[4 + e] += hi[c][e];
+      }
+    }
+    for (int part = 0; part < ad.parts; ++part)
+      *reinterpret_cast<u32x4*>(lds + ((int64_t)part * m * R + i * 8)) = take_part(t);
+  }
+}
+
+constexpr int kAdapterAhead = 2;
+template <int CB>
+struct AdapterFirst {
+  int adapter[kAdapterAhead];              // -1: none
+  uint64_t match[kAdapterAhead];
+  bf16x8 b[kAdapterAhead][CB];             // U of columns n[c], first 32 of the rank
+};
+
+template <int CB>
+__device__ __forceinline__ bf16x8 adapter_u(const AdapterArgs& ad, int adapter, int n_total, int R, int n, int kk) {
+  const __bf16* up = ad.up + ((int64_t)adapter * n_total + n) * R;
+  return keep_or_zero(*reinterpret_cast<const bf16x8*>(up + min(kk, R - 8)), kk < R);
+}
+
+// Wave `share` of `shares` takes the distinct adapters share, share + shares, ...
+template <int CB>
+__device__ __forceinline__ void adapter_first(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
+                                              int share, int shares, AdapterFirst<CB>& first) {
+  const int lane = threadIdx.x & 63, lq = lane >> 4;
+  const int id[1] = {adapter_of(ad.rows, ad.count, lane, m)};
+  AdapterWalk<1> walk(id);
+  int d = -1;
+#pragma unroll
+  for (int i = 0; i < kAdapterAhead; ++i) {
+    first.adapter[i] = -1;
+    first.match[i] = 0;
+    while (walk.next(id)) {
+      if (++d % shares != share) continue;
+      first.adapter[i] = walk.adapter;
+      first.match[i] = walk.match[0];
+      break;
+    }
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      first.b[i][c] = adapter_u<CB>(ad, max(first.adapter[i], 0), n_total, R, n[c], 8 * lq);
+  }
+}
+
+// acc += one adapter's branch for the rows `match`, T's parts in LDS.
+template <int RB, int CB>
+__device__ __forceinline__ void adapter_one(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
+                                            int adapter, uint64_t match, bf16x8 (&b)[CB], const __bf16* lds,
+                                            f32x4 (&acc)[RB][CB]) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
+  for (int j0 = 0; j0 < R; j0 += 32) {
+    const int kk = j0 + 8 * lq, kc = min(kk, R - 8);
+    if (j0 > 0) {
+#pragma unroll
+      for (int c = 0; c < CB; ++c) b[c] = adapter_u<CB>(ad, adapter, n_total, R, n[c], kk);
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const uint32_t mask = (uint32_t)(match >> (16 * rb)) & 0xFFFFu;
+      if (mask == 0) continue;
+      f32x4 sum[CB];
+#pragma unroll
+      for (int c = 0; c < CB; ++c) sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < ad.parts; ++p) {
+        const bf16x8 a = keep_or_zero(
+            *reinterpret_cast<const bf16x8*>(lds + ((int64_t)p * m + min(rb * 16 + lr, m - 1)) * R + kc),
+            kk < R && ((mask >> lr) & 1));
+#pragma unroll
+        for (int c = 0; c < CB; ++c) sum[c] = adapter_mfma(a, b[c], sum[c]);
       }
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        const uint32_t mask = (uint32_t)(walk.match[0] >> (16 * rb)) & 0xFFFFu;
-        if (!mask) continue;
-        float t[8];
-        adapter_t8(ad, min(rb * 16 + lr, m - 1), m, R, kc, t);
-        const bool mine = kok && ((mask >> lr) & 1);
+      for (int i = 0; i < 4; ++i) {
+        const bool mine = (mask >> (4 * lq + i)) & 1;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = mine ? t[e] : 0.0f;
-        adapter_block<CB>(t, b, parts, mask, 0xFFFFu, acc[rb], [&](int e) { return 4 * lq + e; });
+        for (int c = 0; c < CB; ++c) acc[rb][c][i] += mine ? sum[c][i] : 0.0f;
       }
     }
   }
 }
 
-// part[c][i][j] = s_a sum over chunk c's inputs of X[i][k] D_a[j][k], a the
-// adapter of row i, as T^T = D_a X^T (both matrix operands then read 16
-// consecutive bytes).  Workgroup (b, c, z): 16 RR rows, K chunk c (gpc groups
-// of 128), the row block's distinct adapters z, z + gridDim.z, ...  Its waves
-// split the chunk in steps of 32 and are summed through LDS in wave order.
-// Rows without an adapter are not written (no product reads them).
-constexpr int kAdapterWaves = 4;
+template <int RB, int CB>
+__device__ __forceinline__ void adapter_rows16(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
+                                               int share, int shares, AdapterFirst<CB>& first, const __bf16* lds,
+                                               f32x4 (&acc)[RB][CB]) {
+  const int lane = threadIdx.x & 63, lq = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < kAdapterAhead; ++i)
+    if (first.adapter[i] >= 0)
+      adapter_one<RB, CB>(ad, m, n_total, R, n, first.adapter[i], first.match[i], first.b[i], lds, acc);
+  if (first.adapter[kAdapterAhead - 1] < 0) return;
+  const int id[1] = {adapter_of(ad.rows, ad.count, lane, m)};
+  AdapterWalk<1> walk(id);
+  for (int d = 0; walk.next(id); ++d) {
+    if (d % shares != share || d < shares * kAdapterAhead) continue;
+    bf16x8 b[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) b[c] = adapter_u<CB>(ad, walk.adapter, n_total, R, n[c], 8 * lq);
+    adapter_one<RB, CB>(ad, m, n_total, R, n, walk.adapter, walk.match[0], b, lds, acc);
+  }
+}
 
-template <int RBLK, int RR>
-__global__ __launch_bounds__(64 * kAdapterWaves) void adapter_down_kernel(const __bf16* __restrict__ x,
-                                                                          const __bf16* __restrict__ down,
-                                                                          const float* __restrict__ scales,
-                                                                          const int* __restrict__ rows, int count,
-                                                                          float* __restrict__ part, int m, int k,
-                                                                          int r, int gpc) {
-  static_assert(RR * RBLK <= 8 && RR <= 4, "partial tiles in LDS: at most 32 KB; one row id per lane");
-  constexpr int NW = kAdapterWaves;
+// ---------------------------------------------------------------------------
+// T = s_a X D_a^T, as T^T = D_a X^T (both matrix operands then read 16
+// consecutive bytes).  Workgroup (b, c, z): 16 RR rows, K chunk c (gpc groups
+// of 128), the row block's distinct adapters z, z + gridDim.z, ...  Its NW
+// waves split the chunk in steps of 32 and are summed through LDS in wave
+// order.  Rows without an adapter are not written (no product reads them).
+//   PARTS: one chunk; T's bf16 parts to t16 (parts x m x r)
+//   else:  the chunk's float32 sums to part (chunks x m x r)
+// ---------------------------------------------------------------------------
+struct AdapterDown {
+  const __bf16* x;          // m x k
+  const __bf16* down;       // count x r x k
+  const float* scales;      // count
+  const int* rows;          // m
+  float* part;
+  __bf16* t16;
+  int m, k, r, count, chunks, gpc, parts;
+};
+
+template <int RBLK, int RR, int NW, bool PARTS>
+__global__ __launch_bounds__(64 * NW) void adapter_down_kernel(AdapterDown a) {
+  static_assert(RR <= 4 && RR <= NW, "one row id per lane; a wave per row block of the result");
+  static_assert(NW * RR * RBLK <= 128, "partial tiles in LDS: at most 128 KB");
   __shared__ f32x4 red[NW][RR][RBLK][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int lr = lane & 15, lq = lane >> 4;
+  const int m = a.m, k = a.k, r = a.r;
   const int m0 = blockIdx.x * 16 * RR;
-  const int kb = blockIdx.y * gpc * kGroup;                 // chunk start (< k)
-  const int kl = min(gpc * kGroup, k - kb);
-  const int id[1] = {lane < 16 * RR ? adapter_of(rows, count, m0 + lane, m) : -1};
+  const int kb = blockIdx.y * a.gpc * kGroup;               // chunk start (< k)
+  const int kl = min(a.gpc * kGroup, k - kb);
+  const int id[1] = {lane < 16 * RR ? adapter_of(a.rows, a.count, m0 + lane, m) : -1};
   const __bf16* xrow[RR];
 #pragma unroll
-  for (int i = 0; i < RR; ++i) xrow[i] = x + (int64_t)min(m0 + 16 * i + lr, m - 1) * k + kb + 8 * lq;
-  constexpr int LPS = RR + RBLK;                            // loads of one step
-  constexpr int U = LPS <= 3 ? 8 : (LPS <= 5 ? 4 : 2);
-  const int steps = (kl - wave * 32 + 32 * NW - 1) / (32 * NW);
+  for (int i = 0; i < RR; ++i) xrow[i] = a.x + (int64_t)min(m0 + 16 * i + lr, m - 1) * k + kb + 8 * lq;
+  // steps whose loads are in flight together (the loop is bound by their latency)
+  constexpr int LPS = RR + RBLK;
+  constexpr int U = LPS <= 2 ? 8 : (LPS <= 3 ? 6 : (LPS <= 5 ? 4 : 2));
+  const int all = kl / 32;                                  // steps of the chunk; this wave's: wave, wave + NW, ...
   AdapterWalk<1> walk(id);
   for (int d = 0; walk.next(id); d = d + 1 == (int)gridDim.z ? 0 : d + 1) {
     if (d != (int)blockIdx.z) continue;
-    const __bf16* da = down + (int64_t)walk.adapter * r * k + kb + 8 * lq;
+    const __bf16* da = a.down + (int64_t)walk.adapter * r * k + kb + 8 * lq;
     const __bf16* drow[RBLK];
 #pragma unroll
     for (int j = 0; j < RBLK; ++j) drow[j] = da + (int64_t)min(j * 16 + lr, r - 1) * k;
@@ -311,34 +381,24 @@ __global__ __launch_bounds__(64 * kAdapterWaves) void adapter_down_kernel(const 
     for (int i = 0; i < RR; ++i)
 #pragma unroll
       for (int j = 0; j < RBLK; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int st = 0;
-    for (; st + U <= steps; st += U) {
+    for (int st = wave; st < all; st += U * NW) {
       bf16x8 bv[U][RR], av[U][RBLK];
+      // a step past the chunk loads the first one again and is not used
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k0 = wave * 32 + 32 * NW * (st + u);
+        const int k0 = 32 * (st + u * NW < all ? st + u * NW : wave);
 #pragma unroll
         for (int i = 0; i < RR; ++i) bv[u][i] = *reinterpret_cast<const bf16x8*>(xrow[i] + k0);
 #pragma unroll
         for (int j = 0; j < RBLK; ++j) av[u][j] = *reinterpret_cast<const bf16x8*>(drow[j] + k0);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u) {
+        if (st + u * NW >= all) break;
 #pragma unroll
         for (int i = 0; i < RR; ++i)
 #pragma unroll
           for (int j = 0; j < RBLK; ++j) acc[i][j] = mfma16x16x32(av[u][j], bv[u][i], acc[i][j]);
-    }
-    for (; st < steps; ++st) {
-      const int k0 = wave * 32 + 32 * NW * st;
-      bf16x8 b[RR];
-#pragma unroll
-      for (int i = 0; i < RR; ++i) b[i] = *reinterpret_cast<const bf16x8*>(xrow[i] + k0);
-#pragma unroll
-      for (int j = 0; j < RBLK; ++j) {
-        const bf16x8 a = *reinterpret_cast<const bf16x8*>(drow[j] + k0);
-#pragma unroll
-        for (int i = 0; i < RR; ++i) acc[i][j] = mfma16x16x32(a, b[i], acc[i][j]);
       }
     }
 #pragma unroll
@@ -346,25 +406,32 @@ __global__ __launch_bounds__(64 * kAdapterWaves) void adapter_down_kernel(const 
 #pragma unroll
       for (int j = 0; j < RBLK; ++j) red[wave][i][j][lane] = acc[i][j];
     __syncthreads();
-    const float s = scales[walk.adapter];
-    // wave i (< RR) sums and stores row block i, the partials in wave order
+    const float s = a.scales[walk.adapter];
+    // the tiles (row block i, rank block j) go round the waves; partial sums in wave order
+    for (int tile = wave; tile < RR * RBLK; tile += NW) {
+      const int i = tile / RBLK, j = tile - i * RBLK;
+      f32x4 v = red[0][i][j][lane];
 #pragma unroll
-    for (int i = 0; i < RR; ++i) {
-      if (i != wave || !((walk.match[0] >> (16 * i + lr)) & 1)) continue;
+      for (int w = 1; w < NW; ++w) {
+        const f32x4 o = red[w][i][j][lane];
+        v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
+      }
+      v[0] *= s; v[1] *= s; v[2] *= s; v[3] *= s;
       const int mm = m0 + 16 * i + lr;
+      const int rr = j * 16 + 4 * lq;        // rows rr .. rr+3 of T^T; r % 8 == 0, so rr < r implies rr + 3 < r
+      if (!((walk.match[0] >> (16 * i + lr)) & 1) || rr >= r) continue;
+      if constexpr (PARTS) {
+        for (int p = 0; p < a.parts; ++p) {
+          const u32x2 w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          *reinterpret_cast<u32x2*>(a.t16 + ((int64_t)p * m + mm) * r + rr) = w;
 #pragma unroll
-      for (int j = 0; j < RBLK; ++j) {
-        f32x4 v = red[0][i][j][lane];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) {
-          const f32x4 o = red[w][i][j][lane];
-          v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
+          for (int e = 0; e < 2; ++e) {
+            v[2 * e] -= bf16_bits_to_f32(w[e] & 0xFFFFu);
+            v[2 * e + 1] -= __builtin_bit_cast(float, w[e] & 0xFFFF0000u);
+          }
         }
-        const int rr = j * 16 + 4 * lq;      // rows rr .. rr+3 of T^T; r % 8 == 0, so rr < r implies rr + 3 < r
-        if (rr < r) {
-          v[0] *= s; v[1] *= s; v[2] *= s; v[3] *= s;
-          *reinterpret_cast<f32x4*>(part + ((int64_t)blockIdx.y * m + mm) * r + rr) = v;
-        }
+      } else {
+        *reinterpret_cast<f32x4*>(a.part + ((int64_t)blockIdx.y * m + mm) * r + rr) = v;
       }
     }
     __syncthreads();                         // red is free for the next adapter

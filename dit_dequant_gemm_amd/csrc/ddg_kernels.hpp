@@ -242,6 +242,11 @@ __device__ __forceinline__ f32x16 mfma32x32x16(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// The row blocks of a wave as (row block, column block).
+__device__ __forceinline__ f32x16 (&tile_blocks(f32x16 (&acc)[kBM / 32]))[kBM / 32][1] {
+  return reinterpret_cast<f32x16 (&)[kBM / 32][1]>(acc);
+}
+
 // Groups [g0, g1) of the 256 x 256 output tile (tm, tn) of the product
 // `args`, added into acc (8 row blocks of the 32x32 accumulator layout; wave w
 // holds columns 32w..32w+31).  With `lowrank` set, the branch term
@@ -274,6 +279,11 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
   const rsrc_t rx = make_rsrc(args.x + (int64_t)m0 * K, (uint32_t)m_valid * xrow_bytes);
   const rsrc_t rw = make_rsrc(args.packed + (int64_t)nw0 * row_bytes, (uint32_t)n_valid * row_bytes);
   const rsrc_t rs = make_rsrc(args.scales + (int64_t)nw0 * G, (uint32_t)n_valid * G * 4);
+
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    if (lowrank) adapter_tile<32, 1, false>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc));
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
   // X -> LDS.  DMA instruction i (0..7) of wave w fills 1 KB block 8w+i: rows
   // 32w + 4i + lane/16, slot lane%16, holding logical chunk slot ^ (row & 15).
@@ -346,8 +356,7 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
   // their latencies overlap (32760 x 5120 x 5120, r = 32: 1558 -> 1504 us for
   // the fused call); it still adds into acc before the K loop
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    if (lowrank)
-      adapter_tile32(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, m0, min(nw0 + wave * 32 + lr, args.n - 1), acc);
+    if (lowrank) adapter_tile<32, 1, true>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc));
   } else if (lowrank && args.t != nullptr) {
     // acc = T * lora_up^T over the rank dimension, 16 at a time (zero-padded).
     const int R = args.r;
@@ -570,6 +579,11 @@ __device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, 
 #pragma unroll
     for (int c = 0; c < CB; ++c) acc[rb][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    adapter_tile<16, CB, false>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
   uint32_t wc[CB][B], wn[CB][B], be1[CB][B];
   float sc[CB], sn[CB], nsh[CB];
   uint32_t ev[CB], od[CB];              // 4-bit: the chunk dword's codes plus one, as bytes
@@ -614,10 +628,7 @@ __device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, 
   // the low-rank branch behind the first group's loads, as in K2
   // (4096 x 3072 x 3072, r = 32: 87.6 -> 84.3 us for the fused call)
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    int n[CB];
-#pragma unroll
-    for (int c = 0; c < CB; ++c) n[c] = min(nw0 + (int)ncol + 16 * c, args.n - 1);
-    adapter_tile16(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, m0, n, acc);
+    adapter_tile<16, CB, true>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc);
   } else if (args.t != nullptr) {
     // acc = T * lora_up^T over the rank dimension, 32 at a time (zero-padded).
     const int R = args.r;
@@ -1239,6 +1250,11 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
   [&]<int... J>(std::integer_sequence<int, J...>) {
     ((load_x(J, J), load_w(J, J)), ...);
   }(std::make_integer_sequence<int, D>{});
+  // the K splits share out the rows' distinct adapters
+  [[maybe_unused]] const int ad_col[1] = {n};
+  [[maybe_unused]] AdapterFirst<1> first;
+  if constexpr (std::is_same_v<Ad, AdapterArgs>)
+    adapter_first<1>(ad, args.m, args.n, args.r, ad_col, part * NK + h, sp.parts * NK, first);
   // main loop: whole blocks of S steps (every ring index a constant)
   const int full = steps / S * S;
   for (int j0 = 0; j0 < full; j0 += S) {
@@ -1260,12 +1276,15 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
       acc[rb][i] = (acc4[0][rb][i] + acc4[1][rb][i]) + (acc4[2][rb][i] + acc4[3][rb][i]);
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    // the K splits share out the distinct adapters
-    const int nn[1] = {n};
+    // T's parts into the X ring, which every wave is done with
+    static_assert(S * NK * XSLOT >= adapter_stage_bytes(16 * RB), "T's parts fit the X ring");
+    __bf16* t_lds = reinterpret_cast<__bf16*>(&L.xs0[0][0]);
+    adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NC * NK);
+    __syncthreads();
     f32x4 br[RB][1];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) br[rb][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    adapter_rows16<RB, 1>(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, nn, part * NK + h, sp.parts * NK, br);
+    adapter_rows16<RB, 1>(ad, args.m, args.n, args.r, ad_col, part * NK + h, sp.parts * NK, first, t_lds, br);
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -1574,6 +1593,14 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
 #pragma unroll
     for (int d = 0; d < NDMA; ++d) off_cur[d] = off_next[d];
   };
+  // the eight K splits share out the rows' distinct adapters
+  [[maybe_unused]] int ad_col[NCB];
+  [[maybe_unused]] AdapterFirst<NCB> first;
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) ad_col[cb] = min(n0 + cb * 16 + lr, args.n - 1);
+    adapter_first<NCB>(ad, args.m, args.n, args.r, ad_col, wave, NW, first);
+  }
   for (int c0 = 0; c0 < nch; c0 += CU) {
     [&]<int... U>(std::integer_sequence<int, U...>) __attribute__((always_inline)) {
       (chunk_body(integral_constant<int, U>{}, c0 + U), ...);
@@ -1581,15 +1608,17 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
   }
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    // the eight K splits share out the distinct adapters
-    int n[NCB];
     f32x4 br[1][NCB];
 #pragma unroll
-    for (int cb = 0; cb < NCB; ++cb) {
-      n[cb] = min(n0 + cb * 16 + lr, args.n - 1);
-      br[0][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    adapter_rows16<1, NCB>(ad, args.m, args.n, args.r, args.out_bf16 ? 2 : 3, n, wave, NW, br);
+    for (int cb = 0; cb < NCB; ++cb) br[0][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // T's parts into the first weight buffer, once every wave is done with it
+    static_assert(SkinnyLds<B, KC, NCB>::W0 >= adapter_stage_bytes(16), "T's parts fit the first weight buffer");
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    __bf16* t_lds = reinterpret_cast<__bf16*>(wl0);
+    adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NW);
+    __syncthreads();
+    adapter_rows16<1, NCB>(ad, args.m, args.n, args.r, ad_col, wave, NW, first, t_lds, br);
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb)
 #pragma unroll

@@ -62,7 +62,7 @@ hipError_t launch_rpbh_rotate(const void* x, bool f32_in, int64_t n, int d, cons
                               hipStream_t stream);
 
 // The products above with an adapter per row, and the pre-pass that writes
-// ad.t (chunks x m x r float32; chunk c: gpc groups of 128 inputs).
+// their T.
 template <int B>
 hipError_t launch_adapter_large(const GemmArgs& a, const AdapterArgs& ad, hipStream_t stream);
 template <int B>
@@ -78,14 +78,8 @@ hipError_t launch_adapter_small_split(const GemmArgs& a, int nc, const SmallSpli
                                       hipStream_t stream);
 template <int B>
 hipError_t launch_adapter_skinny(const GemmArgs& a, int kc, int ncb, const AdapterArgs& ad, hipStream_t stream);
-struct AdapterDown {
-  const __bf16* x;          // m x k
-  const __bf16* down;       // count x r x k
-  const float* scales;      // count
-  const int* rows;          // m
-  float* t;
-  int m, k, r, count, chunks, gpc;
-};
+// at most this many rows: float32 chunk sums (AdapterArgs::t), else bf16 parts
+constexpr int kAdapterFewRows = 64;
 hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream);
 // Row blocks of 16 per workgroup of a pre-pass for m rows at rank r.
 int lowrank_t_row_blocks(int m, int r);

@@ -299,7 +299,7 @@ int ddg_lowrank_fused_gemm_noalloc(const void* x, int64_t m, int64_t k, const ui
  * T = s_a X[i] D_a^T is summed in float32 and enters the matrix product in
  * bf16 parts that hold it to 2^-16 for a bf16 y and to 2^-24 for a float32 y;
  * the branch is summed into the product's float32 accumulator, rounded once.
- *   workspace  device scratch: T in float32 first (required:
+ *   workspace  device scratch: T first (required:
  *              ddg_adapter_workspace_bytes with split = 0), then optionally
  *              the split-K area of ddg_dequant_gemm (split = 1).  Its contents
  *              are scratch.  Calls that share it must be ordered.  Under graph
@@ -315,9 +315,9 @@ int ddg_adapter_gemm(const void* x, int64_t m, int64_t k, const uint8_t* packed,
                      hipStream_t stream);
 
 /*
- * Workspace bytes of ddg_adapter_gemm: T (M x r float32 for each of at most 8
- * parts of K that the pre-pass spreads over workgroups, rounded up to 256)
- * and, with split != 0, the split-K area of ddg_dequant_gemm.  Host-only.
+ * Workspace bytes of ddg_adapter_gemm: T (M <= 64: M x r float32 for each of
+ * ceil(G / 16), at most 8, parts of the G = K / 128 groups; more rows: three
+ * M x r bf16; rounded up to 256) and, with split != 0, the split-K area of ddg_dequant_gemm.  Host-only.
  * Errors: DDG_ERR_ARG (null), DDG_ERR_SHAPE (m negative or above 2^28 - 16, n
  * negative or above 2^31 - 1, k not a positive multiple of 128 up to 2^20, r
  * outside 8..128 or not a multiple of 8).

@@ -31,11 +31,12 @@ def _up256(b):
 
 
 def test_workspace_bytes(lib):
-    # T in float32, once per K part: at most 8 parts, fewer where the rows
-    # alone give 512 workgroups of 16 rows; parts are whole groups of 128
-    for m, k, parts in [(1, 512, 4), (16, 5120, 8), (64, 13824, 8), (1001, 5120, 8), (4096, 5120, 2),
-                        (8192, 5120, 1), (32760, 5120, 1), (3, 128, 1), (16, 1152, 5)]:
+    # at most 64 rows: T in float32, once per part of K (16 groups of 128 to a
+    # part, at most 8 parts); more rows: three bf16 parts of T
+    for m, k, parts in [(1, 512, 1), (16, 5120, 3), (64, 13824, 7), (64, 1 << 20, 8), (3, 128, 1), (16, 2176, 2)]:
         assert _bytes(lib, m, 256, k, 24) == (OK, _up256(parts * m * 24 * 4)), (m, k)
+    for m in (65, 1001, 32760):
+        assert _bytes(lib, m, 256, 5120, 24) == (OK, _up256(3 * m * 24 * 2)), m
     assert _bytes(lib, 0) == (OK, 0)
     plain = ctypes.c_size_t()
     for m, n, k in [(16, 1024, 8192), (512, 5120, 5120), (16, 15360, 5120)]:
