@@ -937,7 +937,7 @@ int rope_call(const ddg_rope_tensor* q, const ddg_rope_tensor* k, int dtype, int
     ddg::RopeTensor r{};
     if (t)
       r = ddg::RopeTensor{t->x, t->y, t->weight, t->x_batch, t->x_token, t->x_head,
-                          t->y_batch, t->y_token, t->y_head, (int)t->heads};
+                          t->y_batch, t->y_token, t->y_head, (int)t->heads, aligned(t->weight, 16)};
     return r;
   };
   a.q = fill(q);

@@ -96,6 +96,7 @@ struct RopeTensor {
   const void* w;
   int64_t xb, xt, xh, yb, yt, yh;
   int heads;
+  int w_vec;                // w is 16-byte aligned
 };
 struct RopeArgs {
   RopeTensor q, k;

@@ -57,35 +57,43 @@ __device__ __forceinline__ double pair_turns(const RopeArgs& a, const int32_t* p
   return (double)pos[axis] * (a.freqs[p] * 0.15915494309189533577);
 }
 
-// V consecutive values as float32 (the address is a multiple of their bytes).
+// V consecutive values of a row as loaded (the address is a multiple of their
+// bytes), and their conversion.
 template <typename T, int V>
-__device__ __forceinline__ void load_vals(const void* base, int64_t i, float (&f)[V]) {
-  const T* p = static_cast<const T*>(base) + i;
-  if constexpr (sizeof(T) == 4 && V == 4) {
-    const f32x4 t = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = t[j];
-  } else if constexpr (sizeof(T) == 2 && V >= 4) {
-    uint32_t w[V / 2];
-    if constexpr (V == 8) {
+struct Chunk {
+  static constexpr int W = sizeof(T) * V / 4 > 0 ? (int)sizeof(T) * V / 4 : 1;     // dwords
+  uint32_t w[W];
+  __device__ __forceinline__ void load(const void* base, int64_t i) {
+    const T* p = static_cast<const T*>(base) + i;
+    if constexpr (sizeof(T) * V == 16) {
       const u32x4 t = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[j] = t[j];
-    } else {
+    } else if constexpr (sizeof(T) * V == 8) {
       const u32x2 t = *reinterpret_cast<const u32x2*>(p);
       w[0] = t[0];
       w[1] = t[1];
+    } else if constexpr (sizeof(T) == 4) {
+      w[0] = __builtin_bit_cast(uint32_t, (float)*p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-      f[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
-      f[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = (float)p[j];
   }
-}
+  __device__ __forceinline__ void values(float (&f)[V]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[j] = __builtin_bit_cast(float, w[j]);
+    } else if constexpr (V == 1) {
+      f[0] = bf16_bits_to_f32(w[0]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        f[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
+        f[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xFFFF0000u);
+      }
+    }
+  }
+};
 
 template <typename T, int V>
 __device__ __forceinline__ void store_vals(void* base, int64_t i, const float (&f)[V]) {
@@ -103,17 +111,33 @@ __device__ __forceinline__ void store_vals(void* base, int64_t i, const float (&
   }
 }
 
+// V norm weights from entry i on (1 without weights); vec: 16-byte aligned
+// and i a multiple of V.
 template <int V>
-__device__ __forceinline__ void load_weight(const void* w, bool w_f32, int64_t i, float (&f)[V]) {
-  if (w == nullptr) {
+__device__ __forceinline__ void load_weight(const RopeTensor& x, bool w_f32, int64_t i, float (&f)[V]) {
+  if (x.w == nullptr) {
 #pragma unroll
     for (int j = 0; j < V; ++j) f[j] = 1.0f;
   } else if (w_f32) {
+    const float* p = static_cast<const float*>(x.w) + i;
+    if (V >= 4 && x.w_vec) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = static_cast<const float*>(w)[i + j];
+      for (int j = 0; j < V / 4; ++j) {
+        const f32x4 t = *reinterpret_cast<const f32x4*>(p + 4 * j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[4 * j + e] = t[e];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[j] = p[j];
+    }
+  } else if (V >= 4 && x.w_vec) {
+    Chunk<__bf16, V> t;
+    t.load(x.w, i);
+    t.values(f);
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) f[j] = bf16_bits_to_f32(static_cast<const uint16_t*>(w)[i + j]);
+    for (int j = 0; j < V; ++j) f[j] = bf16_bits_to_f32(static_cast<const uint16_t*>(x.w)[i + j]);
   }
 }
 
@@ -187,8 +211,13 @@ __device__ __forceinline__ float run_sum(float v, int lg) {
   return v;
 }
 
-__device__ __forceinline__ float rstd_of(float sum, int count, float eps) {
-  return 1.0f / __builtin_sqrtf(sum / (float)count + eps);
+// 1 / sqrt(v): the hardware's estimate (within an ulp) and one Newton step,
+// the library's root where the step could leave the normal range.
+__device__ __forceinline__ float rsqrt_of(float v) {
+  if (!(v > 0x1p-100f && v < 0x1p100f)) return 1.0f / __builtin_sqrtf(v);
+  const float y = __builtin_amdgcn_rsqf(v);
+  const float h = __builtin_fmaf(-v * y, y, 1.0f);             // 1 - v y^2
+  return __builtin_fmaf(0.5f * y, h, y);
 }
 
 constexpr int kRopeWaves = 4;
@@ -196,21 +225,41 @@ constexpr int kRopeWaves = 4;
 // No norm, or the norm over each head.  A wave takes one token (or, with
 // splits > 1, one of `splits` shares of its heads): 2^lg lanes per head, one
 // slot per lane, 64 >> lg heads at a time, query heads first.  V = 1 gives a
-// head to the whole wave, up to NS slots per lane.
+// head to the whole wave, up to NS slots per lane.  The next heads' values
+// are loaded before the current ones are turned, the first ones before the
+// angles are computed.
 template <typename T, int V, bool HALF, bool NORM>
 __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) {
   constexpr int NS = V == 1 ? kRopeMaxHeadDim / 128 : 1;
-  constexpr int U = V == 1 ? 1 : 2;                       // head groups in flight
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sl = lane & ((1 << a.lg) - 1), hl = lane >> a.lg, hpw = 64 >> a.lg;
   const int slots = a.dim / (2 * V);
   const int gq = (a.q.heads + hpw - 1) / hpw, gk = (a.k.heads + hpw - 1) / hpw, groups = gq + gk;
   const int64_t total = (int64_t)a.batch * a.tokens * a.splits;
+  const float inv_dim = 1.0f / (float)a.dim;
   for (int64_t w = (int64_t)blockIdx.x * kRopeWaves + wave; w < total; w += (int64_t)gridDim.x * kRopeWaves) {
     const int row = (int)(w / a.splits), part = (int)(w - (int64_t)row * a.splits);
     const int b = row / a.tokens, t = row - b * a.tokens;
     const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
+    const int g0 = (int)((int64_t)part * groups / a.splits), g1 = (int)((int64_t)(part + 1) * groups / a.splits);
+
+    Chunk<T, V> next[NS][2];
+    auto load_group = [&](int g) {
+      const bool is_q = g < gq;
+      const RopeTensor& x = is_q ? a.q : a.k;
+      // heads past the last: the last again, not stored
+      const int h = min((g - (is_q ? 0 : gq)) * hpw + hl, x.heads - 1);
+      const int64_t base = (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const Slot<V, HALF> k(a, min(sl + 64 * i, slots - 1));
+        next[i][0].load(x.x, base + k.ia);
+        next[i][1].load(x.x, base + k.ib);
+      }
+    };
+    load_group(g0);
+
     float c[NS][V], s[NS][V];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -230,174 +279,191 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
         }
       }
     }
-    const int g0 = (int)((int64_t)part * groups / a.splits), g1 = (int)((int64_t)(part + 1) * groups / a.splits);
-    for (int g = g0; g < g1; g += U) {
-      float fa[U][NS][V], fb[U][NS][V];
-      bool ok[U];
+
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool is_q = g + u < gq;
-        const RopeTensor& x = is_q ? a.q : a.k;
-        const int h = (g + u - (is_q ? 0 : gq)) * hpw + hl;
-        ok[u] = g + u < g1 && h < x.heads;
-        const int64_t base = (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
+    for (int z = 0; z < 2; ++z) {
+      const RopeTensor& x = z ? a.k : a.q;
+      const int first = z ? gq : 0;                    // the tensor's first group
+      const int lo = max(g0, first), hi = min(g1, z ? groups : gq);
+      if (lo >= hi) continue;
+      float wa[NS][V], wb[NS][V];
+      if constexpr (NORM) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          const int slot = sl + 64 * i;
-          if (ok[u] && slot < slots) {
-            const Slot<V, HALF> k(a, slot);
-            load_vals<T, V>(x.x, base + k.ia, fa[u][i]);
-            load_vals<T, V>(x.x, base + k.ib, fb[u][i]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) fa[u][i][j] = fb[u][i][j] = 0.0f;
-          }
+          const Slot<V, HALF> k(a, min(sl + 64 * i, slots - 1));
+          load_weight<V>(x, a.w_f32, k.ia, wa[i]);
+          load_weight<V>(x, a.w_f32, k.ib, wb[i]);
         }
       }
+      for (int g = lo; g < hi; ++g) {
+        float fa[NS][V], fb[NS][V];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool is_q = g + u < gq;
-        const RopeTensor& x = is_q ? a.q : a.k;
-        const int h = (g + u - (is_q ? 0 : gq)) * hpw + hl;
-        float rstd = 1.0f;
+        for (int i = 0; i < NS; ++i) {
+          next[i][0].values(fa[i]);
+          next[i][1].values(fb[i]);
+        }
+        if (g + 1 < g1) load_group(g + 1);
+        const int h = (g - first) * hpw + hl;
         if constexpr (NORM) {
           float sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < NS; ++i)
+          for (int i = 0; i < NS; ++i) {
+            float part_sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j)
-              sum = __builtin_fmaf(fa[u][i][j], fa[u][i][j], __builtin_fmaf(fb[u][i][j], fb[u][i][j], sum));
-          rstd = rstd_of(run_sum(sum, a.lg), a.dim, a.eps);
+              part_sum = __builtin_fmaf(fa[i][j], fa[i][j], __builtin_fmaf(fb[i][j], fb[i][j], part_sum));
+            sum += sl + 64 * i < slots ? part_sum : 0.0f;
+          }
+          const float rstd = rsqrt_of(__builtin_fmaf(run_sum(sum, a.lg), inv_dim, a.eps));
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              fa[i][j] = fa[i][j] * rstd * wa[i][j];
+              fb[i][j] = fb[i][j] * rstd * wb[i][j];
+            }
         }
         const int64_t base = (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const int slot = sl + 64 * i;
-          if (!ok[u] || slot >= slots) continue;
           const Slot<V, HALF> k(a, slot);
-          if constexpr (NORM) {
-            float wa[V], wb[V];
-            load_weight<V>(x.w, a.w_f32, k.ia, wa);
-            load_weight<V>(x.w, a.w_f32, k.ib, wb);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              fa[u][i][j] = fa[u][i][j] * rstd * wa[j];
-              fb[u][i][j] = fb[u][i][j] * rstd * wb[j];
-            }
-          }
-          if (k.turns) turn_slot<V, HALF>(fa[u][i], fb[u][i], c[i], s[i]);
-          store_vals<T, V>(x.y, base + k.ia, fa[u][i]);
-          store_vals<T, V>(x.y, base + k.ib, fb[u][i]);
+          if (slot >= slots || h >= x.heads) continue;
+          if (k.turns) turn_slot<V, HALF>(fa[i], fb[i], c[i], s[i]);
+          store_vals<T, V>(x.y, base + k.ia, fa[i]);
+          store_vals<T, V>(x.y, base + k.ib, fb[i]);
         }
       }
     }
   }
 }
 
-// The norm over all heads of a token: a workgroup takes one token, its lanes
-// the (head, slot) items in order; the sums of squares of q and of k are
-// joined through LDS in wave order, and the token's cosines and sines are
-// computed once into LDS.  The first kHold items of a lane stay in registers
-// between the two passes; later ones are read again (from the L2).
+// The norm over all heads of a token: a workgroup takes q (blockIdx.y = 0) or
+// k of one token after another, its lanes the (head, slot) items in order, NH
+// each; the sums of squares are joined through LDS in wave order, and the
+// token's cosines and sines are computed once into LDS.  The weights of a
+// lane's items stay in registers over the tokens, and the next token's values
+// are loaded before the current one is finished.  Items past a lane's NH (more
+// than 1024 slots) are read twice, the second time from the L2.
 constexpr int kRopeMaxWaves = 8;
-template <typename T, int V, bool HALF>
+template <typename T, int V, bool HALF, int NH>
 __global__ __launch_bounds__(64 * kRopeMaxWaves) void rope_token_kernel(RopeArgs a) {
-  constexpr int kHold = V == 1 ? 4 : 2;
-  __shared__ float cs[2][kRopeMaxHeadDim / 2];
+  __shared__ float cs[2][2][kRopeMaxHeadDim / 2];
   __shared__ float part[2][kRopeMaxWaves];
   const int tid = threadIdx.x, n = blockDim.x, lane = tid & 63, wave = tid >> 6, waves = n >> 6;
-  const int slots = a.dim / (2 * V);
-  for (int64_t row = blockIdx.x; row < (int64_t)a.batch * a.tokens; row += gridDim.x) {
+  const RopeTensor x = blockIdx.y ? a.k : a.q;
+  const int slots = a.dim / (2 * V), items = x.heads * slots;
+  const int64_t rows = (int64_t)a.batch * a.tokens;
+  auto at = [&](bool out, int64_t row, int h) -> int64_t {
     const int b = (int)(row / a.tokens), t = (int)(row - (int64_t)b * a.tokens);
-    const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
-    float fa[2][kHold][V], fb[2][kHold][V];
-    float sum[2] = {0.0f, 0.0f};
-    auto load_item = [&](const RopeTensor& x, int item, float (&va)[V], float (&vb)[V]) {
-      const int h = item / slots, slot = item - h * slots;
+    return out ? (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh
+               : (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
+  };
+  int head[NH], slot_of[NH];                     // items past the last: head -1
+  float wa[NH][V], wb[NH][V];
+#pragma unroll
+  for (int i = 0; i < NH; ++i) {
+    const int item = tid + i * n;
+    head[i] = item < items ? item / slots : -1;
+    slot_of[i] = item % slots;
+    if (head[i] < 0) continue;
+    const Slot<V, HALF> k(a, slot_of[i]);
+    load_weight<V>(x, a.w_f32, (int64_t)head[i] * a.dim + k.ia, wa[i]);
+    load_weight<V>(x, a.w_f32, (int64_t)head[i] * a.dim + k.ib, wb[i]);
+  }
+  Chunk<T, V> next[NH][2];
+  auto load_token = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      if (head[i] < 0) continue;
+      const Slot<V, HALF> k(a, slot_of[i]);
+      const int64_t base = at(false, row, head[i]);
+      next[i][0].load(x.x, base + k.ia);
+      next[i][1].load(x.x, base + k.ib);
+    }
+  };
+  auto squares = [&](const float (&va)[V], const float (&vb)[V], float acc) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc = __builtin_fmaf(va[j], va[j], __builtin_fmaf(vb[j], vb[j], acc));
+    return acc;
+  };
+  if ((int64_t)blockIdx.x < rows) load_token(blockIdx.x);
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
+    if (a.pairs > 0) {
+      const int b = (int)(row / a.tokens), t = (int)(row - (int64_t)b * a.tokens);
+      const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
+      for (int p = tid; p < a.pairs; p += n) {
+        float c, s;
+        cos_sin_turns(pair_turns(a, pos, p), c, s);
+        cs[buf][0][p] = c * a.amplitude;
+        cs[buf][1][p] = s * a.signed_amplitude;
+      }
+    }
+    float fa[NH][V], fb[NH][V];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      if (head[i] < 0) continue;
+      next[i][0].values(fa[i]);
+      next[i][1].values(fb[i]);
+      sum = squares(fa[i], fb[i], sum);
+    }
+    for (int item = tid + NH * n; item < items; item += n) {
+      const int h = item / slots;
+      const Slot<V, HALF> k(a, item - h * slots);
+      Chunk<T, V> ca, cb;
+      ca.load(x.x, at(false, row, h) + k.ia);
+      cb.load(x.x, at(false, row, h) + k.ib);
+      float va[V], vb[V];
+      ca.values(va);
+      cb.values(vb);
+      sum = squares(va, vb, sum);
+    }
+    if (row + gridDim.x < rows) load_token(row + gridDim.x);
+    sum = run_sum(sum, 6);
+    if (lane == 0) part[buf][wave] = sum;
+    lds_barrier();               // one per token: the next one writes the other cs and part
+    float all = 0.0f;
+    for (int i = 0; i < waves; ++i) all += part[buf][i];
+    const float rstd = rsqrt_of(all / (float)(x.heads * a.dim) + a.eps);
+    auto finish = [&](int h, int slot, float (&va)[V], float (&vb)[V], const float (&ua)[V], const float (&ub)[V]) {
       const Slot<V, HALF> k(a, slot);
-      const int64_t base = (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
-      load_vals<T, V>(x.x, base + k.ia, va);
-      load_vals<T, V>(x.x, base + k.ib, vb);
-    };
-    auto finish_item = [&](const RopeTensor& x, int item, float rstd, float (&va)[V], float (&vb)[V]) {
-      const int h = item / slots, slot = item - h * slots;
-      const Slot<V, HALF> k(a, slot);
-      float wa[V], wb[V];
-      load_weight<V>(x.w, a.w_f32, (int64_t)h * a.dim + k.ia, wa);
-      load_weight<V>(x.w, a.w_f32, (int64_t)h * a.dim + k.ib, wb);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        va[j] = va[j] * rstd * wa[j];
-        vb[j] = vb[j] * rstd * wb[j];
+        va[j] = va[j] * rstd * ua[j];
+        vb[j] = vb[j] * rstd * ub[j];
       }
       if (k.turns) {
         float c[V], s[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int p = k.pair(slot, j);
-          c[j] = cs[0][p];
-          s[j] = cs[1][p];
+          c[j] = cs[buf][0][p];
+          s[j] = cs[buf][1][p];
         }
         turn_slot<V, HALF>(va, vb, c, s);
       }
-      const int64_t base = (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh;
+      const int64_t base = at(true, row, h);
       store_vals<T, V>(x.y, base + k.ia, va);
       store_vals<T, V>(x.y, base + k.ib, vb);
     };
-    auto squares = [&](const float (&va)[V], const float (&vb)[V], float acc) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc = __builtin_fmaf(va[j], va[j], __builtin_fmaf(vb[j], vb[j], acc));
-      return acc;
-    };
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const RopeTensor& x = z ? a.k : a.q;
-      const int items = x.heads * slots;
-#pragma unroll
-      for (int i = 0; i < kHold; ++i) {
-        const int item = tid + i * n;
-        if (item < items) load_item(x, item, fa[z][i], fb[z][i]);
-      }
+    for (int i = 0; i < NH; ++i)
+      if (head[i] >= 0) finish(head[i], slot_of[i], fa[i], fb[i], wa[i], wb[i]);
+    for (int item = tid + NH * n; item < items; item += n) {
+      const int h = item / slots, slot = item - h * slots;
+      const Slot<V, HALF> k(a, slot);
+      Chunk<T, V> ca, cb;
+      ca.load(x.x, at(false, row, h) + k.ia);
+      cb.load(x.x, at(false, row, h) + k.ib);
+      float va[V], vb[V], ua[V], ub[V];
+      ca.values(va);
+      cb.values(vb);
+      load_weight<V>(x, a.w_f32, (int64_t)h * a.dim + k.ia, ua);
+      load_weight<V>(x, a.w_f32, (int64_t)h * a.dim + k.ib, ub);
+      finish(h, slot, va, vb, ua, ub);
     }
-    for (int p = tid; p < a.pairs; p += n) {
-      float c, s;
-      cos_sin_turns(pair_turns(a, pos, p), c, s);
-      cs[0][p] = c * a.amplitude;
-      cs[1][p] = s * a.signed_amplitude;
-    }
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const RopeTensor& x = z ? a.k : a.q;
-      const int items = x.heads * slots;
-#pragma unroll
-      for (int i = 0; i < kHold; ++i)
-        if (tid + i * n < items) sum[z] = squares(fa[z][i], fb[z][i], sum[z]);
-      for (int item = tid + kHold * n; item < items; item += n) {
-        float va[V], vb[V];
-        load_item(x, item, va, vb);
-        sum[z] = squares(va, vb, sum[z]);
-      }
-      sum[z] = run_sum(sum[z], 6);
-      if (lane == 0) part[z][wave] = sum[z];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const RopeTensor& x = z ? a.k : a.q;
-      const int items = x.heads * slots;
-      float all = 0.0f;
-      for (int i = 0; i < waves; ++i) all += part[z][i];
-      const float rstd = rstd_of(all, x.heads * a.dim, a.eps);
-#pragma unroll
-      for (int i = 0; i < kHold; ++i)
-        if (tid + i * n < items) finish_item(x, tid + i * n, rstd, fa[z][i], fb[z][i]);
-      for (int item = tid + kHold * n; item < items; item += n) {
-        float va[V], vb[V];
-        load_item(x, item, va, vb);
-        finish_item(x, item, rstd, va, vb);
-      }
-    }
-    __syncthreads();                       // cs and part are free for the next token
   }
 }
 
@@ -406,12 +472,19 @@ hipError_t launch_v(RopeArgs a, int norm, int cus, hipStream_t stream) {
   const int slots = a.dim / (2 * V);
   const int64_t rows = (int64_t)a.batch * a.tokens;
   if (norm == DDG_NORM_TOKEN) {
-    // lanes in whole waves, the same number of items for nearly all of them
+    // lanes in whole waves, the same number of items (one or two) for nearly
+    // all of them; as many workgroups as are resident at once
     const int64_t items = (int64_t)std::max(a.q.heads, a.k.heads) * slots;
-    const int64_t per = (items + 64 * kRopeMaxWaves - 1) / (64 * kRopeMaxWaves);
-    const int lanes = (int)(((items + per - 1) / per + 63) / 64 * 64);
-    const int64_t grid = std::min<int64_t>(rows, (int64_t)cus * 64);
-    rope_token_kernel<T, V, HALF><<<dim3((unsigned)grid), dim3((unsigned)lanes), 0, stream>>>(a);
+    const int64_t most = 64 * kRopeMaxWaves;
+    const int64_t per = std::min<int64_t>((items + most - 1) / most, 2);
+    const int lanes = (int)std::min<int64_t>(((items + per - 1) / per + 63) / 64 * 64, most);
+    const int tensors = a.k.heads > 0 ? 2 : 1;
+    const int64_t grid = std::min<int64_t>(rows, (int64_t)cus * std::max(1, 16 * 64 / lanes / tensors));
+    const dim3 blocks((unsigned)grid, (unsigned)tensors);
+    if (per == 1)
+      rope_token_kernel<T, V, HALF, 1><<<blocks, dim3((unsigned)lanes), 0, stream>>>(a);
+    else
+      rope_token_kernel<T, V, HALF, 2><<<blocks, dim3((unsigned)lanes), 0, stream>>>(a);
     return hipGetLastError();
   }
   a.lg = 0;
