@@ -79,6 +79,12 @@ struct Chunk {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
+  // the words as they are: values() after it converts again, where the
+  // compiler would keep the first conversion's twice as many registers
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int j = 0; j < W; ++j) asm("" : "+v"(w[j]));
+  }
   __device__ __forceinline__ void values(float (&f)[V]) const {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -145,8 +151,8 @@ __device__ __forceinline__ void load_weight(const RopeTensor& x, bool w_f32, int
 // below P / V hold the rotated part: chunk a at V slot, chunk b P further on,
 // so that in the half layout the pairs are (a[j], b[j]) and in the
 // interleaved one lie inside the chunks (V = 1: the pair itself).  The other
-// slots hold the rest of the head, 2V values each.  P and D / 2 are multiples
-// of V.
+// slots hold the rest of the head in the same way, its first half and its
+// second.  P and D / 2 are multiples of V.
 template <int V, bool HALF>
 struct Slot {
   int ia, ib;
@@ -154,8 +160,8 @@ struct Slot {
   __device__ __forceinline__ Slot(const RopeArgs& a, int slot) {
     turns = slot * V < a.pairs;
     if (!turns) {
-      ia = slot * 2 * V;
-      ib = ia + V;
+      ia = a.pairs + slot * V;
+      ib = a.dim / 2 + slot * V;
     } else if (V == 1 && !HALF) {
       ia = 2 * slot;
       ib = ia + 1;
@@ -222,6 +228,40 @@ __device__ __forceinline__ float rsqrt_of(float v) {
 
 constexpr int kRopeWaves = 4;
 
+// A token's cosines and sines, one pair per lane (all of a wave's lanes at
+// once would compute each pair once per head group, 8 times at 128 values per
+// head), handed to the lanes that need them through the wave's own LDS.
+struct WaveAngles {
+  __attribute__((aligned(16))) float c[kRopeMaxHeadDim / 2], s[kRopeMaxHeadDim / 2];
+  __device__ __forceinline__ void compute(const RopeArgs& a, const int32_t* pos, int lane) {
+    for (int p = lane; p < a.pairs; p += 64) {
+      float cp, sp;
+      cos_sin_turns(pair_turns(a, pos, p), cp, sp);
+      c[p] = cp * a.amplitude;
+      s[p] = sp * a.signed_amplitude;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+  template <int V, bool HALF>
+  __device__ __forceinline__ void take(const Slot<V, HALF>& k, int slot, float (&fc)[V], float (&fs)[V]) const {
+    // runs of R consecutive pairs, aligned to R
+    constexpr int R = HALF || V == 1 ? (V < 4 ? V : 4) : V / 2;
+    typedef float run __attribute__((ext_vector_type(R)));
+#pragma unroll
+    for (int j = 0; j < V; j += R) {
+      const int p = k.pair(slot, j);
+      const run rc = *reinterpret_cast<const run*>(c + p), rs = *reinterpret_cast<const run*>(s + p);
+#pragma unroll
+      for (int e = 0; e < R; ++e) {
+        fc[j + e] = rc[e];
+        fs[j + e] = rs[e];
+      }
+    }
+  }
+};
+
 // No norm, or the norm over each head.  A wave takes one token (or, with
 // splits > 1, one of `splits` shares of its heads): 2^lg lanes per head, one
 // slot per lane, 64 >> lg heads at a time, query heads first.  V = 1 gives a
@@ -231,6 +271,7 @@ constexpr int kRopeWaves = 4;
 template <typename T, int V, bool HALF, bool NORM>
 __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) {
   constexpr int NS = V == 1 ? kRopeMaxHeadDim / 128 : 1;
+  __shared__ WaveAngles ang[kRopeWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int sl = lane & ((1 << a.lg) - 1), hl = lane >> a.lg, hpw = 64 >> a.lg;
@@ -260,24 +301,13 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
     };
     load_group(g0);
 
+    ang[wave].compute(a, pos, lane);
     float c[NS][V], s[NS][V];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int slot = sl + 64 * i;
       const Slot<V, HALF> k(a, slot);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        c[i][j] = 1.0f;
-        s[i][j] = 0.0f;
-      }
-      if (slot < slots && k.turns) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          cos_sin_turns(pair_turns(a, pos, k.pair(slot, j)), c[i][j], s[i][j]);
-          c[i][j] *= a.amplitude;
-          s[i][j] *= a.signed_amplitude;
-        }
-      }
+      if (slot < slots && k.turns) ang[wave].template take<V, HALF>(k, slot, c[i], s[i]);
     }
 
 #pragma unroll
@@ -334,6 +364,71 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
           store_vals<T, V>(x.y, base + k.ib, fb[i]);
         }
       }
+    }
+  }
+}
+
+// The norm over all heads of a token where one wave can hold q (or k) of a
+// token: job 2 row + z is tensor z of token row, its lanes as in the head
+// kernel, G groups of heads in registers between the sum of squares and the
+// rotation.  No barrier, and every wave's loads are all in flight at once.
+template <typename T, int V, bool HALF, int G>
+__global__ __launch_bounds__(64 * kRopeWaves) void rope_token_wave_kernel(RopeArgs a) {
+  __shared__ WaveAngles ang[kRopeWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int slots = a.dim / (2 * V);
+  const int sl = lane & ((1 << a.lg) - 1), hl = lane >> a.lg, hpw = 64 >> a.lg;
+  const int tensors = a.k.heads > 0 ? 2 : 1;
+  const int64_t total = (int64_t)a.batch * a.tokens * tensors;
+  for (int64_t w = (int64_t)blockIdx.x * kRopeWaves + wave; w < total; w += (int64_t)gridDim.x * kRopeWaves) {
+    const int row = (int)(w / tensors);
+    const RopeTensor& x = w - (int64_t)row * tensors ? a.k : a.q;
+    const int b = row / a.tokens, t = row - b * a.tokens;
+    const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
+    const Slot<V, HALF> k(a, min(sl, slots - 1));
+    Chunk<T, V> raw[G][2];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      // heads past the last: the last again, neither summed nor stored
+      const int64_t base = (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)min(g * hpw + hl, x.heads - 1) * x.xh;
+      raw[g][0].load(x.x, base + k.ia);
+      raw[g][1].load(x.x, base + k.ib);
+    }
+    ang[wave].compute(a, pos, lane);
+    float sum = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float fa[V], fb[V], part = 0.0f;
+      raw[g][0].values(fa);
+      raw[g][1].values(fb);
+#pragma unroll
+      for (int j = 0; j < V; ++j) part = __builtin_fmaf(fa[j], fa[j], __builtin_fmaf(fb[j], fb[j], part));
+      sum += sl < slots && g * hpw + hl < x.heads ? part : 0.0f;
+    }
+    const float rstd = rsqrt_of(run_sum(sum, 6) / (float)(x.heads * a.dim) + a.eps);
+    float c[V], s[V];
+    if (sl < slots && k.turns) ang[wave].template take<V, HALF>(k, sl, c, s);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int h = g * hpw + hl;
+      if (sl >= slots || h >= x.heads) continue;
+      raw[g][0].keep();
+      raw[g][1].keep();
+      float fa[V], fb[V], wa[V], wb[V];
+      raw[g][0].values(fa);
+      raw[g][1].values(fb);
+      load_weight<V>(x, a.w_f32, (int64_t)h * a.dim + k.ia, wa);
+      load_weight<V>(x, a.w_f32, (int64_t)h * a.dim + k.ib, wb);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        fa[j] = fa[j] * rstd * wa[j];
+        fb[j] = fb[j] * rstd * wb[j];
+      }
+      if (k.turns) turn_slot<V, HALF>(fa, fb, c, s);
+      const int64_t base = (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh;
+      store_vals<T, V>(x.y, base + k.ia, fa);
+      store_vals<T, V>(x.y, base + k.ib, fb);
     }
   }
 }
@@ -471,14 +566,29 @@ template <typename T, int V, bool HALF>
 hipError_t launch_v(RopeArgs a, int norm, int cus, hipStream_t stream) {
   const int slots = a.dim / (2 * V);
   const int64_t rows = (int64_t)a.batch * a.tokens;
+  a.lg = 0;
+  while ((1 << a.lg) < slots && a.lg < 6) ++a.lg;
+  const int hpw = 64 >> a.lg;
   if (norm == DDG_NORM_TOKEN) {
+    const int tensors = a.k.heads > 0 ? 2 : 1;
+    const int most_heads = std::max(a.q.heads, a.k.heads);
+    if constexpr (V > 1) {
+      const int groups = (most_heads + hpw - 1) / hpw;
+      const int64_t grid = std::min<int64_t>((rows * tensors + kRopeWaves - 1) / kRopeWaves, (int64_t)cus * 64);
+      auto launch = [&](auto kernel) {
+        kernel<<<dim3((unsigned)grid), dim3(64 * kRopeWaves), 0, stream>>>(a);
+        return hipGetLastError();
+      };
+      if (groups <= 2) return launch(rope_token_wave_kernel<T, V, HALF, 2>);
+      if (groups <= 5) return launch(rope_token_wave_kernel<T, V, HALF, 5>);
+      if (groups <= 8) return launch(rope_token_wave_kernel<T, V, HALF, 8>);
+    }
     // lanes in whole waves, the same number of items (one or two) for nearly
     // all of them; as many workgroups as are resident at once
-    const int64_t items = (int64_t)std::max(a.q.heads, a.k.heads) * slots;
+    const int64_t items = (int64_t)most_heads * slots;
     const int64_t most = 64 * kRopeMaxWaves;
     const int64_t per = std::min<int64_t>((items + most - 1) / most, 2);
     const int lanes = (int)std::min<int64_t>(((items + per - 1) / per + 63) / 64 * 64, most);
-    const int tensors = a.k.heads > 0 ? 2 : 1;
     const int64_t grid = std::min<int64_t>(rows, (int64_t)cus * std::max(1, 16 * 64 / lanes / tensors));
     const dim3 blocks((unsigned)grid, (unsigned)tensors);
     if (per == 1)
@@ -487,9 +597,6 @@ hipError_t launch_v(RopeArgs a, int norm, int cus, hipStream_t stream) {
       rope_token_kernel<T, V, HALF, 2><<<blocks, dim3((unsigned)lanes), 0, stream>>>(a);
     return hipGetLastError();
   }
-  a.lg = 0;
-  while ((1 << a.lg) < slots && a.lg < 6) ++a.lg;
-  const int hpw = 64 >> a.lg;
   const int groups = (a.q.heads + hpw - 1) / hpw + (a.k.heads + hpw - 1) / hpw;
   // a token's heads go to several waves while tokens alone leave waves idle
   const int64_t want = (int64_t)cus * 16;
