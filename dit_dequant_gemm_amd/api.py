@@ -313,73 +313,79 @@ def rope_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", fac
     return torch.tensor(list(out), dtype=torch.float64, device=device), amplitude.value
 
 
-def _heads_view(t: torch.Tensor, name: str, like=None):
-    """(tensor as batch x tokens x heads x dim, strides) of a 3-D or 4-D GPU
-    tensor whose last dimension is dense."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{name} must be bf16 or float32")
-    if t.dim() not in (3, 4):
+_ROPE_DTYPES = {torch.bfloat16: DDG_BF16, torch.float32: DDG_F32}
+_DENSE = torch.contiguous_format
+
+
+def _rope_tensor(x: torch.Tensor, out: Optional[torch.Tensor], weight, name: str):
+    """(RopeTensor, output) of heads x (3-D or 4-D, the last dimension dense)
+    and its output, a new dense tensor where out is None."""
+    st = x.stride()
+    shape = x.shape
+    n = len(st)
+    if not x.is_cuda or x.dtype not in _ROPE_DTYPES:
+        raise ValueError(f"{name} must be a bf16 or float32 GPU tensor")
+    if n not in (3, 4):
         raise ValueError(f"{name} must be ([batch,] tokens, heads, head_dim)")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be dense")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} has the wrong shape, dtype or device")
-    st = t.stride()
-    return (st[0], st[1], st[2]) if t.dim() == 4 else (0, st[0], st[1])
-
-
-def _rope_tensor(x: torch.Tensor, out: Optional[torch.Tensor], weight: Optional[torch.Tensor], name: str):
-    xs = _heads_view(x, name)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    ys = _heads_view(out, f"out of {name}", x)
-    return RopeTensor(x.data_ptr(), out.data_ptr(), None if weight is None else weight.data_ptr(), x.shape[-2],
-                      *xs, *ys), out
+        out = torch.empty_like(x, memory_format=_DENSE)
+        ot = out.stride()
+    else:
+        ot = out.stride()
+        if out.shape != shape or out.dtype != x.dtype or out.device != x.device:
+            raise ValueError(f"out of {name} has the wrong shape, dtype or device")
+        if ot[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"out of {name}: the last dimension must be dense")
+    w = None if weight is None else weight.data_ptr()
+    if n == 4:
+        return RopeTensor(x.data_ptr(), out.data_ptr(), w, shape[2], st[0], st[1], st[2], ot[0], ot[1], ot[2]), out
+    return RopeTensor(x.data_ptr(), out.data_ptr(), w, shape[1], 0, st[0], st[1], 0, ot[0], ot[1]), out
 
 
 def _rope_desc(x: torch.Tensor, positions, freqs, layout: str, sections, amplitude: float, inverse: bool):
-    """(RopeDesc, tensors it points into) for heads x, its positions checked
-    against x's batch and tokens."""
-    if layout not in ROPE_LAYOUTS:
+    """RopeDesc for heads x, the positions checked against x's batch and
+    tokens; and the batch and tokens."""
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
-    d = RopeDesc(axes=1, layout=ROPE_LAYOUTS[layout], inverse=int(bool(inverse)), amplitude=amplitude)
+    xs = x.shape
+    batch, tokens = (xs[0], xs[1]) if len(xs) == 4 else (1, xs[0])
+    d = RopeDesc(axes=1, layout=code, inverse=1 if inverse else 0, amplitude=amplitude)
     if freqs is None:
         if positions is not None or sections is not None:
             raise ValueError("positions and sections need freqs")
-        return d
+        return d, batch, tokens
     if positions is None:
         raise ValueError("freqs need positions")
-    for t, name in ((positions, "positions"), (freqs, "freqs")):
-        _require_cuda(t, name)
-        if t.device != x.device:
-            raise ValueError(f"{name} must be on the device of the heads")
-    if freqs.dtype != torch.float64 or freqs.dim() != 1:
-        raise ValueError("freqs must be a 1-D float64 tensor")
-    if positions.dtype != torch.int32:
-        raise ValueError("positions must be int32")
+    dev = x.get_device()
+    if positions.get_device() != dev or freqs.get_device() != dev:
+        raise ValueError("positions and freqs must be on the GPU of the heads")
+    if freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a dense 1-D float64 tensor")
+    if positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise ValueError("positions must be dense int32")
     pairs = freqs.shape[0]
-    sections = (pairs,) if sections is None else tuple(int(s) for s in sections)
-    if not 1 <= len(sections) <= ROPE_MAX_AXES or min(sections) < 0 or sum(sections) != pairs:
-        raise ValueError(f"sections must be 1 to {ROPE_MAX_AXES} pair counts that add up to len(freqs)")
-    batch, tokens = (x.shape[0], x.shape[1]) if x.dim() == 4 else (1, x.shape[0])
-    axes = len(sections)
+    if sections is None:
+        axes = 1
+        d.sections[0] = pairs
+    else:
+        axes = len(sections)
+        if not 1 <= axes <= ROPE_MAX_AXES or min(sections) < 0 or sum(sections) != pairs:
+            raise ValueError(f"sections must be 1 to {ROPE_MAX_AXES} pair counts that add up to len(freqs)")
+        for i, n in enumerate(sections):
+            d.sections[i] = n
     shape = tuple(positions.shape)
-    if axes == 1 and shape in ((tokens,), (tokens, 1)):
-        per_batch = False
-    elif axes > 1 and shape == (tokens, axes):
-        per_batch = False
-    elif x.dim() == 4 and (shape == (batch, tokens, axes) or (axes == 1 and shape == (batch, tokens))):
-        per_batch = True
+    if shape == (tokens, axes) or (axes == 1 and shape == (tokens,)):
+        per_batch = 0
+    elif len(xs) == 4 and (shape == (batch, tokens, axes) or (axes == 1 and shape == (batch, tokens))):
+        per_batch = tokens * axes
     else:
         raise ValueError("positions must be (tokens, axes) or (batch, tokens, axes)")
-    d.positions, d.freqs = positions.data_ptr(), freqs.data_ptr()
-    d.positions_batch = tokens * axes if per_batch else 0
+    d.positions, d.freqs, d.positions_batch = positions.data_ptr(), freqs.data_ptr(), per_batch
     d.axes, d.rot_dim = axes, 2 * pairs
-    for i, s in enumerate(sections):
-        d.sections[i] = s
-    return d
+    return d, batch, tokens
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout: str = "interleaved",
@@ -391,15 +397,21 @@ def rope(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout: 
     rope_frequencies).  positions: int32 (tokens,) or (tokens, axes), or the
     same with a leading batch; sections: pairs of each axis.  inverse turns
     back (the gradient of the rotation).  out may be x itself."""
+    if freqs is None:
+        raise ValueError("rope needs positions and freqs")
     with _device_of(x):
         t, out = _rope_tensor(x, out, None, "x")
-        if freqs is None:
-            raise ValueError("rope needs positions and freqs")
-        d = _rope_desc(x, positions, freqs, layout, sections, amplitude, inverse)
-        batch, tokens = (x.shape[0], x.shape[1]) if x.dim() == 4 else (1, x.shape[0])
-        _check(load_library().ddg_rope(ctypes.byref(t), DDG_F32 if x.dtype == torch.float32 else DDG_BF16, batch,
-                                       tokens, x.shape[-1], ctypes.byref(d), _stream_ptr(x.device)), "ddg_rope")
+        d, batch, tokens = _rope_desc(x, positions, freqs, layout, sections, amplitude, inverse)
+        _check(load_library().ddg_rope(t, _ROPE_DTYPES[x.dtype], batch, tokens, x.shape[-1], d,
+                                       _stream_ptr(x.device)), "ddg_rope")
     return out
+
+
+def _norm_weight(w: torch.Tensor, t: torch.Tensor, norm: str, name: str) -> torch.dtype:
+    size = t.shape[-1] * t.shape[-2] if norm == "token" else t.shape[-1]
+    if w.dtype not in _ROPE_DTYPES or w.numel() != size or w.get_device() != t.get_device() or not w.is_contiguous():
+        raise ValueError(f"{name} must hold {size} dense bf16 or float32 values on the GPU of the heads")
+    return w.dtype
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -413,36 +425,30 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     rounding.  q and k may have different head counts (k may be None); both
     may be slices of the fused projection's output, and each may be its own
     output.  freqs None: the norms alone."""
-    if norm not in ROPE_NORMS:
+    code = ROPE_NORMS.get(norm)
+    if code is None:
         raise ValueError(f"norm must be one of {sorted(ROPE_NORMS)}")
-    if k is not None and (k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]
-                          or k.dtype != q.dtype or k.device != q.device):
-        raise ValueError("q and k must agree but for their head counts")
-    if k is None and (k_weight is not None or out_k is not None):
-        raise ValueError("k_weight and out_k need k")
-    wdt = None
-    for w, t, name in ((q_weight, q, "q_weight"), (k_weight, k, "k_weight")):
-        if w is None:
-            continue
-        _require_cuda(w, name)
-        size = t.shape[-1] * (t.shape[-2] if norm == "token" else 1)
-        if w.dtype not in (torch.bfloat16, torch.float32) or w.numel() != size or w.device != q.device:
-            raise ValueError(f"{name} must hold {size} bf16 or float32 values on the device of q")
-        if wdt not in (None, w.dtype):
-            raise ValueError("q_weight and k_weight must have one dtype")
-        wdt = w.dtype
     with _device_of(q):
         tq, out_q = _rope_tensor(q, out_q, q_weight, "q")
+        wdt = None if q_weight is None else _norm_weight(q_weight, q, norm, "q_weight")
         tk = None
         if k is not None:
+            qs, ks = q.shape, k.shape
+            if len(ks) != len(qs) or ks[:-2] != qs[:-2] or ks[-1] != qs[-1] or k.dtype != q.dtype or \
+                    k.get_device() != q.get_device():
+                raise ValueError("q and k must agree but for their head counts")
             tk, out_k = _rope_tensor(k, out_k, k_weight, "k")
-        d = _rope_desc(q, positions, freqs, layout, sections, amplitude, False)
-        batch, tokens = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
+            if k_weight is not None:
+                kdt = _norm_weight(k_weight, k, norm, "k_weight")
+                if wdt not in (None, kdt):
+                    raise ValueError("q_weight and k_weight must have one dtype")
+                wdt = kdt
+        elif k_weight is not None or out_k is not None:
+            raise ValueError("k_weight and out_k need k")
+        d, batch, tokens = _rope_desc(q, positions, freqs, layout, sections, amplitude, False)
         _check(load_library().ddg_qk_norm_rope(
-            ctypes.byref(tq), None if tk is None else ctypes.byref(tk),
-            DDG_F32 if q.dtype == torch.float32 else DDG_BF16, DDG_F32 if wdt == torch.float32 else DDG_BF16,
-            batch, tokens, q.shape[-1], ROPE_NORMS[norm], eps, ctypes.byref(d), _stream_ptr(q.device)),
-            "ddg_qk_norm_rope")
+            tq, tk, _ROPE_DTYPES[q.dtype], DDG_BF16 if wdt is torch.bfloat16 else DDG_F32, batch, tokens,
+            q.shape[-1], code, eps, d, _stream_ptr(q.device)), "ddg_qk_norm_rope")
     return out_q, out_k
 
 
@@ -772,29 +778,31 @@ def adapter_gemm(x: torch.Tensor, qw: QWeight, pool: AdapterPool, rows: torch.Te
     by default each call takes its own from torch's allocator.  Under graph
     capture K is not split (see dequant_gemm)."""
     x = _prep_x(x, qw)
-    _require_cuda(rows, "rows")
-    m, r = x.shape[0], pool.down.shape[1]
-    if rows.dtype != torch.int32 or rows.shape != (m,):
-        raise ValueError("rows must be int32, one entry per row of x")
-    if pool.down.shape[2] != qw.k or pool.up.shape[1] != qw.n:
+    m, k, n, dev = x.shape[0], qw.k, qw.n, x.get_device()
+    down, up = pool.down, pool.up
+    adapters, r, pk = down.shape
+    if rows.dtype != torch.int32 or rows.shape != (m,) or not rows.is_contiguous():
+        raise ValueError("rows must be dense int32, one entry per row of x")
+    if pk != k or up.shape[1] != n:
         raise ValueError("the pool does not fit the weight")
-    y = _out(x, qw.n, out_dtype, out)
-    for t in (rows, pool.down, qw.packed, qw.scales, y):
-        if t.device != x.device:
-            raise ValueError("every tensor must be on the device of x")
+    y = _out(x, n, out_dtype, out)
+    if rows.get_device() != dev or down.get_device() != dev or qw.packed.get_device() != dev or y.get_device() != dev:
+        raise ValueError("rows, the pool, the weight and out must be on the GPU of x")
     with _device_of(x):
         split = not _capturing()
         if workspace is None:
-            workspace = torch.empty(max(256, adapter_workspace_bytes(m, qw.n, qw.k, r, split)), dtype=torch.uint8,
-                                    device=x.device)
+            wbytes = adapter_workspace_bytes(m, n, k, r, split)
+            workspace = torch.empty(wbytes or 256, dtype=torch.uint8, device=x.device)
         else:
             _require_cuda(workspace, "workspace")
-        wbytes = workspace.numel() * workspace.element_size()
-        if not split:
-            wbytes = min(wbytes, adapter_workspace_bytes(m, qw.n, qw.k, r, False))
+            if workspace.get_device() != dev:
+                raise ValueError("workspace must be on the GPU of x")
+            wbytes = workspace.numel() * workspace.element_size()
+            if not split:
+                wbytes = min(wbytes, adapter_workspace_bytes(m, n, k, r, False))
         _check(load_library().ddg_adapter_gemm(
-            x.data_ptr(), m, qw.k, qw.packed.data_ptr(), qw.scales.data_ptr(), qw.bits, qw.n, pool.down.data_ptr(),
-            pool.up.data_ptr(), pool.scales.data_ptr(), pool.down.shape[0], r, rows.data_ptr(), y.data_ptr(),
+            x.data_ptr(), m, k, qw.packed.data_ptr(), qw.scales.data_ptr(), qw.bits, n, down.data_ptr(),
+            up.data_ptr(), pool.scales.data_ptr(), adapters, r, rows.data_ptr(), y.data_ptr(),
             DDG_F32 if y.dtype == torch.float32 else DDG_BF16, workspace.data_ptr(), wbytes,
             _stream_ptr(x.device)), "ddg_adapter_gemm")
     return y
