@@ -73,41 +73,44 @@ hipError_t launch_adapter_skinny<DDG_BITS>(const GemmArgs& a, int kc, int ncb, c
 
 #if DDG_BITS == 4
 namespace {
-template <int RBLK, int RR, int NW, bool PARTS>
-hipError_t launch_down(const AdapterDown& d, int z, hipStream_t stream) {
-  const dim3 grid((unsigned)((d.m + 16 * RR - 1) / (16 * RR)), (unsigned)d.chunks, (unsigned)z);
-  adapter_down_kernel<RBLK, RR, NW, PARTS><<<grid, dim3(64 * NW), 0, stream>>>(d);
+template <int RBLK, int RR, bool PARTS>
+hipError_t launch_down(AdapterDown d, int z, hipStream_t stream) {
+  const int blocks = (d.m + 16 * RR - 1) / (16 * RR);
+  // few row blocks: all of them before the next z; many: runs of 8, one per
+  // XCD, so that a block's second adapter starts beside its first
+  d.z = z;
+  d.run = blocks < 64 ? blocks : 8;
+  const int parts = ((d.r + 15) / 16 + RBLK - 1) / RBLK;
+  const dim3 grid((unsigned)((blocks + d.run - 1) / d.run * d.run * z), (unsigned)d.chunks, (unsigned)parts);
+  adapter_down_kernel<RBLK, RR, PARTS><<<grid, dim3(64 * adapter_down_waves(RR, RBLK)), 0, stream>>>(d);
   return hipGetLastError();
 }
 
 template <int RBLK>
-hipError_t launch_rblk(const AdapterDown& d, hipStream_t stream) {
-  // at most 64 rows: every distinct adapter of a row block in a workgroup of its own
-  if (d.m <= kAdapterFewRows) return launch_down<RBLK, 1, 16, false>(d, std::min(d.count, 16), stream);
-  // a block's second adapter goes to a second workgroup: blocks with a
-  // request's end inside would otherwise take twice as long as the others
-  const int rr = lowrank_t_row_blocks(d.m, d.r);
-  if constexpr (RBLK <= 2) {
-    if (rr == 4) return launch_down<RBLK, 4, 8, true>(d, std::min(d.count, 2), stream);
-  }
-  if constexpr (RBLK <= 4) {
-    if (rr == 2) return launch_down<RBLK, 2, 8, true>(d, std::min(d.count, 2), stream);
-  }
-  return launch_down<RBLK, 1, 16, true>(d, std::min(d.count, 2), stream);
+hipError_t launch_rblk(const AdapterDown& d, int rr, int z, hipStream_t stream) {
+  if (rr == 4) return launch_down<RBLK, 4, true>(d, z, stream);
+  if (rr == 2) return launch_down<RBLK, 2, true>(d, z, stream);
+  return launch_down<RBLK, 1, true>(d, z, stream);
 }
 }  // namespace
 
 hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream) {
-  switch ((d.r + 15) / 16) {
-    case 1: return launch_rblk<1>(d, stream);
-    case 2: return launch_rblk<2>(d, stream);
-    case 3: return launch_rblk<3>(d, stream);
-    case 4: return launch_rblk<4>(d, stream);
-    case 5: return launch_rblk<5>(d, stream);
-    case 6: return launch_rblk<6>(d, stream);
-    case 7: return launch_rblk<7>(d, stream);
-    case 8: return launch_rblk<8>(d, stream);
-    default: return hipErrorInvalidValue;
+  // at most 64 rows: every distinct adapter of a row block and every 16 of
+  // the rank in a workgroup of its own
+  if (d.m <= kAdapterFewRows) return launch_down<1, 1, false>(d, std::min(d.count, 16), stream);
+  // a block's second adapter goes to a second workgroup: blocks with a
+  // request's end inside would otherwise take twice as long as the others
+  const int z = std::min(d.count, 2);
+  const int blocks = (d.m + 15) / 16;
+  if (blocks < 128) return launch_down<1, 1, true>(d, z, stream);
+  // D is read once per workgroup: several row blocks to one while every
+  // compute unit gets a workgroup
+  const int rr = blocks >= 4 * 256 ? 4 : (blocks >= 2 * 256 ? 2 : 1);
+  switch (std::min((d.r + 15) / 16, 4)) {
+    case 1: return launch_rblk<1>(d, rr, z, stream);
+    case 2: return launch_rblk<2>(d, rr, z, stream);
+    case 3: return launch_rblk<3>(d, rr, z, stream);
+    default: return launch_rblk<4>(d, rr, z, stream);
   }
 }
 #endif

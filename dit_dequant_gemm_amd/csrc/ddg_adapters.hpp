@@ -331,11 +331,18 @@ __device__ __forceinline__ void adapter_rows16(const AdapterArgs& ad, int m, int
 }
 
 // ---------------------------------------------------------------------------
-// T = s_a X D_a^T, as T^T = D_a X^T (both matrix operands then read 16
-// consecutive bytes).  Workgroup (b, c, z): 16 RR rows, K chunk c (gpc groups
-// of 128), the row block's distinct adapters z, z + gridDim.z, ...  Its NW
-// waves split the chunk in steps of 32 and are summed through LDS in wave
-// order.  Rows without an adapter are not written (no product reads them).
+// T = s_a X D_a^T, as T^T = D_a X^T.  Workgroup (b, z; c; p): 16 RR rows, the
+// row block's distinct adapters z, z + Z, ..., K chunk c (gpc groups of 128),
+// rank blocks of 16 from p RBLK on.  Its NW waves take runs of the chunk in
+// steps of 64 inputs and are summed through LDS in wave order.
+// A step's rows (X's and D's, 128 bytes each) go HBM -> LDS with buffer_load
+// ... lds, eight whole lines per instruction, into the wave's own two stages;
+// the operands are read back from there.  (Loaded straight into the operand
+// layout, neighbouring lanes read different rows, 16 bytes of a line each, and
+// the line accesses bound the kernel: 32760 x 5120 at rank 32 took 128 us, with
+// the rows read once more 222.)  Row r's 16-byte piece c sits in slot
+// c ^ (r & 7), so that the operand reads spread over the banks.
+// Rows without an adapter are not written (no product reads them).
 //   PARTS: one chunk; T's bf16 parts to t16 (parts x m x r)
 //   else:  the chunk's float32 sums to part (chunks x m x r)
 // ---------------------------------------------------------------------------
@@ -347,78 +354,126 @@ struct AdapterDown {
   float* part;
   __bf16* t16;
   int m, k, r, count, chunks, gpc, parts;
+  int z;                    // workgroups per row block
+  int run;                  // row blocks in a row before the next z
 };
 
-template <int RBLK, int RR, int NW, bool PARTS>
-__global__ __launch_bounds__(64 * NW) void adapter_down_kernel(AdapterDown a) {
-  static_assert(RR <= 4 && RR <= NW, "one row id per lane; a wave per row block of the result");
-  static_assert(NW * RR * RBLK <= 128, "partial tiles in LDS: at most 128 KB");
-  __shared__ f32x4 red[NW][RR][RBLK][64];
+// Waves per workgroup for a step of RR + RBLK row blocks (two stages of 2 KB
+// per row block and wave, at most 128 KB).
+constexpr int adapter_down_waves(int rr, int rblk) { return rr + rblk <= 2 ? 16 : (rr + rblk <= 4 ? 8 : 4); }
+
+template <int RBLK, int RR, bool PARTS>
+__global__ __launch_bounds__(64 * adapter_down_waves(RR, RBLK)) void adapter_down_kernel(AdapterDown a) {
+  constexpr int NW = adapter_down_waves(RR, RBLK);
+  constexpr int ROWS = 16 * (RR + RBLK), STAGE = ROWS * 128;           // bytes of a step
+  static_assert(RR <= 4 && RBLK <= 4, "one row id per lane; stages and partial tiles in LDS");
+  static_assert(RR * RBLK * 1024 <= STAGE, "the partial tiles fit the first stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[NW][STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[NW][STAGE];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int m = a.m, k = a.k, r = a.r;
-  const int m0 = blockIdx.x * 16 * RR;
+  const int runs = blockIdx.x / a.run, z = runs % a.z;
+  const int m0 = (runs / a.z * a.run + (blockIdx.x - runs * a.run)) * 16 * RR;
+  if (m0 >= m) return;
+  const int r0 = blockIdx.z * 16 * RBLK;
   const int kb = blockIdx.y * a.gpc * kGroup;               // chunk start (< k)
   const int kl = min(a.gpc * kGroup, k - kb);
   const int id[1] = {lane < 16 * RR ? adapter_of(a.rows, a.count, m0 + lane, m) : -1};
-  const __bf16* xrow[RR];
+  // this wave's steps of the chunk: a run of its own
+  const int s0 = wave * (kl / 64) / NW, s1 = (wave + 1) * (kl / 64) / NW;
+  const uint32_t row_bytes = (uint32_t)k * 2;
+  // rows past M and ranks past r lie past their resource: zeros
+  const rsrc_t rx = make_rsrc(a.x + (int64_t)m0 * k, (uint32_t)min(16 * RR, m - m0) * row_bytes);
+  const uint32_t piece = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16;    // of row lane / 8 (rows 8 i + lane / 8)
+  const uint32_t lane_off = (uint32_t)(lane >> 3) * row_bytes + piece;
+  uint32_t at[2];                                           // this lane's operand halves within a row block
 #pragma unroll
-  for (int i = 0; i < RR; ++i) xrow[i] = a.x + (int64_t)min(m0 + 16 * i + lr, m - 1) * k + kb + 8 * lq;
-  // steps whose loads are in flight together (the loop is bound by their latency)
-  constexpr int LPS = RR + RBLK;
-  constexpr int U = LPS <= 2 ? 8 : (LPS <= 3 ? 6 : (LPS <= 5 ? 4 : 2));
-  const int all = kl / 32;                                  // steps of the chunk; this wave's: wave, wave + NW, ...
+  for (int h = 0; h < 2; ++h) at[h] = (uint32_t)(lr * 128 + (((2 * lq + h) ^ (lr & 7)) * 16));
+
   AdapterWalk<1> walk(id);
-  for (int d = 0; walk.next(id); d = d + 1 == (int)gridDim.z ? 0 : d + 1) {
-    if (d != (int)blockIdx.z) continue;
-    const __bf16* da = a.down + (int64_t)walk.adapter * r * k + kb + 8 * lq;
-    const __bf16* drow[RBLK];
-#pragma unroll
-    for (int j = 0; j < RBLK; ++j) drow[j] = da + (int64_t)min(j * 16 + lr, r - 1) * k;
+  for (int d = 0; walk.next(id); d = d + 1 == a.z ? 0 : d + 1) {
+    if (d != z) continue;
+    const rsrc_t rd = make_rsrc(a.down + ((int64_t)walk.adapter * r + r0) * k, (uint32_t)min(16 * RBLK, r - r0) * row_bytes);
     f32x4 acc[RR][RBLK];
 #pragma unroll
     for (int i = 0; i < RR; ++i)
 #pragma unroll
       for (int j = 0; j < RBLK; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int st = wave; st < all; st += U * NW) {
-      bf16x8 bv[U][RR], av[U][RBLK];
-      // a step past the chunk loads the first one again and is not used
+    // step st into a stage; past the run, its first step again (not used)
+    auto issue = [&](uint8_t* stage, int st) __attribute__((always_inline)) {
+      const uint32_t soff = (uint32_t)(kb + 64 * (st < s1 ? st : s0)) * 2;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k0 = 32 * (st + u * NW < all ? st + u * NW : wave);
+      for (int i = 0; i < 2 * RR; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_ptr_t)(stage + i * 1024), 16,
+                                                 lane_off + (uint32_t)(8 * i) * row_bytes, soff, 0, 0);
 #pragma unroll
-        for (int i = 0; i < RR; ++i) bv[u][i] = *reinterpret_cast<const bf16x8*>(xrow[i] + k0);
+      for (int i = 0; i < 2 * RBLK; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (lds_ptr_t)(stage + (2 * RR + i) * 1024), 16,
+                                                 lane_off + (uint32_t)(8 * i) * row_bytes, soff, 0, 0);
+    };
+    auto compute = [&](const uint8_t* stage) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < RBLK; ++j) av[u][j] = *reinterpret_cast<const bf16x8*>(drow[j] + k0);
-      }
+      for (int h = 0; h < 2; ++h) {
+        bf16x8 bv[RR], av[RBLK];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (st + u * NW >= all) break;
+        for (int i = 0; i < RR; ++i) bv[i] = *reinterpret_cast<const bf16x8*>(stage + i * 2048 + at[h]);
+#pragma unroll
+        for (int j = 0; j < RBLK; ++j) av[j] = *reinterpret_cast<const bf16x8*>(stage + (RR + j) * 2048 + at[h]);
 #pragma unroll
         for (int i = 0; i < RR; ++i)
 #pragma unroll
-          for (int j = 0; j < RBLK; ++j) acc[i][j] = mfma16x16x32(av[u][j], bv[u][i], acc[i][j]);
+          for (int j = 0; j < RBLK; ++j) acc[i][j] = mfma16x16x32(av[j], bv[i], acc[i][j]);
+      }
+    };
+    constexpr int NI = 2 * (RR + RBLK);                     // loads of a step
+    // all but the last step's loads have landed (the fence keeps the reads below)
+    auto landed = [&] {
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (NI & 15) | ((NI >> 4) << 14));
+      asm volatile("" ::: "memory");
+    };
+    // this wave's reads of a stage are done before loads overwrite it
+    auto read = [&] {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);
+    };
+    if (s0 < s1) {
+      issue(&st0[wave][0], s0);
+      for (int st = s0; st < s1; st += 2) {
+        read();
+        issue(&st1[wave][0], st + 1);
+        landed();
+        compute(&st0[wave][0]);
+        if (st + 1 >= s1) break;
+        read();
+        issue(&st0[wave][0], st + 2);
+        landed();
+        compute(&st1[wave][0]);
       }
     }
+    // the partial tiles go where the first stages were
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(&st0[0][0]);      // [wave][row block][rank block][lane]
 #pragma unroll
     for (int i = 0; i < RR; ++i)
 #pragma unroll
-      for (int j = 0; j < RBLK; ++j) red[wave][i][j][lane] = acc[i][j];
+      for (int j = 0; j < RBLK; ++j) red[((wave * RR + i) * RBLK + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     const float s = a.scales[walk.adapter];
     // the tiles (row block i, rank block j) go round the waves; partial sums in wave order
     for (int tile = wave; tile < RR * RBLK; tile += NW) {
       const int i = tile / RBLK, j = tile - i * RBLK;
-      f32x4 v = red[0][i][j][lane];
+      f32x4 v = red[tile * 64 + lane];
 #pragma unroll
       for (int w = 1; w < NW; ++w) {
-        const f32x4 o = red[w][i][j][lane];
+        const f32x4 o = red[(w * RR * RBLK + tile) * 64 + lane];
         v[0] += o[0]; v[1] += o[1]; v[2] += o[2]; v[3] += o[3];
       }
       v[0] *= s; v[1] *= s; v[2] *= s; v[3] *= s;
       const int mm = m0 + 16 * i + lr;
-      const int rr = j * 16 + 4 * lq;        // rows rr .. rr+3 of T^T; r % 8 == 0, so rr < r implies rr + 3 < r
+      const int rr = r0 + j * 16 + 4 * lq;   // rows rr .. rr+3 of T^T; r % 8 == 0, so rr < r implies rr + 3 < r
       if (!((walk.match[0] >> (16 * i + lr)) & 1) || rr >= r) continue;
       if constexpr (PARTS) {
         for (int p = 0; p < a.parts; ++p) {
@@ -434,7 +489,7 @@ __global__ __launch_bounds__(64 * NW) void adapter_down_kernel(AdapterDown a) {
         *reinterpret_cast<f32x4*>(a.part + ((int64_t)blockIdx.y * m + mm) * r + rr) = v;
       }
     }
-    __syncthreads();                         // red is free for the next adapter
+    __syncthreads();                         // the stages are free for the next adapter
   }
 }
 

@@ -81,8 +81,6 @@ hipError_t launch_adapter_skinny(const GemmArgs& a, int kc, int ncb, const Adapt
 // at most this many rows: float32 chunk sums (AdapterArgs::t), else bf16 parts
 constexpr int kAdapterFewRows = 64;
 hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream);
-// Row blocks of 16 per workgroup of a pre-pass for m rows at rank r.
-int lowrank_t_row_blocks(int m, int r);
 
 // Rotary positions of q (and, with k.heads > 0, k), behind a norm or alone.
 // Strides in elements; w: norm weights (head: dim values, token: heads x dim)
