@@ -1082,6 +1082,8 @@ __global__ __launch_bounds__(512, 1) void gemm_streamk_kernel(GemmArgs args, Str
 // per slot, so that the compiler can see that a DMA into one slot does not
 // alias reads of another, and does not make the reads wait for it) and the
 // partial tiles of the K-split reduction.  A kernel declares it __shared__.
+constexpr size_t kLdsLimit = 160 * 1024;
+
 template <int RB, int NC, int NK>
 struct SmallLds {
   static constexpr int XSLOT = RB * 16 * 256;        // one group's X slice: 16*RB rows x 256 bytes
@@ -1122,10 +1124,20 @@ struct SmallSplit {
 };
 constexpr int kSmallMaxParts = 8;
 
+// T's parts have LDS of their own, written before the K loop, where the other
+// arrays leave room for the workgroups that the grid gives a compute unit (one
+// with NC = 1, else two; the kernel with K split over workgroups has more);
+// else they go over the X ring after it.
+template <int RB, int NC, int NK>
+constexpr bool small_adapter_early() {
+  constexpr size_t lds = sizeof(SmallLds<RB, NC, NK>), all = lds + adapter_stage_bytes(16 * RB);
+  return NK > 1 && all <= kLdsLimit && (NC == 1 || kLdsLimit / all >= 2 || kLdsLimit / lds < 2);
+}
+
 template <int B, int RB, int NC, int NK, typename Ad = NoAdapters>
 __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLds<RB, NC, NK>& L,
                                            const SmallSplit& sp = SmallSplit{nullptr, nullptr, 0, 1},
-                                           int part = 0, const Ad& ad = Ad{}) {
+                                           int part = 0, const Ad& ad = Ad{}, __bf16* t_early = nullptr) {
   // X slices and packed weights of step j + D are loaded into registers at
   // step j (rings of S = D + 1 slots); at step j each wave writes its share of
   // X(j) to the LDS slot, and one LDS barrier hands the slot to the other
@@ -1255,6 +1267,8 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
   [[maybe_unused]] AdapterFirst<1> first;
   if constexpr (std::is_same_v<Ad, AdapterArgs>)
     adapter_first<1>(ad, args.m, args.n, args.r, ad_col, part * NK + h, sp.parts * NK, first);
+  if constexpr (std::is_same_v<Ad, AdapterArgs> && small_adapter_early<RB, NC, NK>())
+    adapter_stage(ad, args.m, args.r, t_early, threadIdx.x, 64 * NC * NK);     // (barriers follow)
   // main loop: whole blocks of S steps (every ring index a constant)
   const int full = steps / S * S;
   for (int j0 = 0; j0 < full; j0 += S) {
@@ -1276,11 +1290,14 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
       acc[rb][i] = (acc4[0][rb][i] + acc4[1][rb][i]) + (acc4[2][rb][i] + acc4[3][rb][i]);
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    // T's parts into the X ring, which every wave is done with
-    static_assert(S * NK * XSLOT >= adapter_stage_bytes(16 * RB), "T's parts fit the X ring");
-    __bf16* t_lds = reinterpret_cast<__bf16*>(&L.xs0[0][0]);
-    adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NC * NK);
-    __syncthreads();
+    __bf16* t_lds = t_early;
+    if constexpr (!small_adapter_early<RB, NC, NK>()) {
+      // into the X ring, which every wave is done with
+      static_assert(S * NK * XSLOT >= adapter_stage_bytes(16 * RB), "T's parts fit the X ring");
+      t_lds = reinterpret_cast<__bf16*>(&L.xs0[0][0]);
+      adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NC * NK);
+      __syncthreads();
+    }
     f32x4 br[RB][1];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) br[rb][0] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1385,7 +1402,9 @@ __global__ __launch_bounds__(64 * NC * NK) void gemm_small_kernel(GemmArgs args)
 template <int B, int RB, int NC, int NK>
 __global__ __launch_bounds__(64 * NC * NK) void gemm_small_adapter_kernel(GemmArgs args, AdapterArgs ad) {
   __shared__ SmallLds<RB, NC, NK> L;
-  small_body<B, RB, NC, NK>(args, blockIdx.x, L, SmallSplit{nullptr, nullptr, 0, 1}, 0, ad);
+  constexpr bool early = small_adapter_early<RB, NC, NK>();
+  __shared__ __attribute__((aligned(16))) __bf16 t_early[early ? adapter_stage_bytes(16 * RB) / 2 : 8];
+  small_body<B, RB, NC, NK>(args, blockIdx.x, L, SmallSplit{nullptr, nullptr, 0, 1}, 0, ad, t_early);
 }
 
 // M <= 16 with K split across workgroups: workgroup id = wg * parts + part.
@@ -1401,7 +1420,9 @@ __global__ __launch_bounds__(64 * NC) void gemm_small_split_adapter_kernel(GemmA
                                                                            AdapterArgs ad) {
   __shared__ SmallLds<1, NC, 1> L;
   const int wg = blockIdx.x / sp.parts, part = blockIdx.x - wg * sp.parts;
-  small_body<B, 1, NC, 1>(args, wg, L, sp, part, ad);
+  constexpr bool early = small_adapter_early<1, NC, 1>();
+  __shared__ __attribute__((aligned(16))) __bf16 t_early[early ? adapter_stage_bytes(16 * 1) / 2 : 8];
+  small_body<B, 1, NC, 1>(args, wg, L, sp, part, ad, t_early);
 }
 
 // ---------------------------------------------------------------------------
@@ -1434,7 +1455,6 @@ __host__ __device__ constexpr size_t skinny_static_lds(int b, int kc, int ncb) {
              : (size_t)8 * ((kc * b + 3) / 4) * 1024 + (size_t)8 * ncb * 1024;
 }
 __host__ __device__ constexpr size_t skinny_scale_lds(int kc) { return (size_t)8 * kc * 64 * 4; }
-constexpr size_t kLdsLimit = 160 * 1024;
 
 // LDS layout of the skinny kernel body: two weight buffers (separate arrays,
 // so that the compiler can tell that a DMA into one does not feed reads of
@@ -1453,9 +1473,16 @@ struct SkinnyLds {
 // Workgroup wg of the product `args` (see the comment above).  wl0, wl1 and
 // scw are LDS arrays of at least SkinnyLds<B, KC, NCB>::W0, ::W1 bytes and
 // [8][KC][64] floats.
+// T's parts before the K loop, in LDS of their own, where there is room.
+template <int B, int KC, int NCB>
+constexpr bool skinny_adapter_early() {
+  return SkinnyLds<B, KC, NCB>::W0 + SkinnyLds<B, KC, NCB>::W1 + skinny_scale_lds(KC) + adapter_stage_bytes(16) <=
+         kLdsLimit;
+}
+
 template <int B, int KC, int NCB, typename Ad = NoAdapters>
 __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_t* wl0, uint8_t* wl1,
-                                            float (*scw)[KC][64], const Ad& ad = Ad{}) {
+                                            float (*scw)[KC][64], const Ad& ad = Ad{}, __bf16* t_early = nullptr) {
   constexpr int NW = SkinnyLds<B, KC, NCB>::NW;       // waves = K splits
   constexpr uint32_t kNoLoad = 0x80000000u;
   constexpr int NDMA = SkinnyLds<B, KC, NCB>::NDMA;
@@ -1600,6 +1627,7 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb) ad_col[cb] = min(n0 + cb * 16 + lr, args.n - 1);
     adapter_first<NCB>(ad, args.m, args.n, args.r, ad_col, wave, NW, first);
+    if constexpr (skinny_adapter_early<B, KC, NCB>()) adapter_stage(ad, args.m, args.r, t_early, threadIdx.x, 64 * NW);
   }
   for (int c0 = 0; c0 < nch; c0 += CU) {
     [&]<int... U>(std::integer_sequence<int, U...>) __attribute__((always_inline)) {
@@ -1611,12 +1639,15 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
     f32x4 br[1][NCB];
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb) br[0][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // T's parts into the first weight buffer, once every wave is done with it
-    static_assert(SkinnyLds<B, KC, NCB>::W0 >= adapter_stage_bytes(16), "T's parts fit the first weight buffer");
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    __bf16* t_lds = reinterpret_cast<__bf16*>(wl0);
-    adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NW);
+    __bf16* t_lds = t_early;
+    if constexpr (!skinny_adapter_early<B, KC, NCB>()) {
+      // into the first weight buffer, once every wave is done with it
+      static_assert(SkinnyLds<B, KC, NCB>::W0 >= adapter_stage_bytes(16), "T's parts fit the first weight buffer");
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      t_lds = reinterpret_cast<__bf16*>(wl0);
+      adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NW);
+    }
     __syncthreads();
     adapter_rows16<1, NCB>(ad, args.m, args.n, args.r, ad_col, wave, NW, first, t_lds, br);
 #pragma unroll
@@ -1680,7 +1711,9 @@ __global__ __launch_bounds__(512) void gemm_skinny_adapter_kernel(GemmArgs args,
   __shared__ __attribute__((aligned(1024))) uint8_t wl0[L::W0];
   __shared__ __attribute__((aligned(1024))) uint8_t wl1[L::W1];
   __shared__ __attribute__((aligned(256))) float scw[L::NW][KC][64];
-  skinny_body<B, KC, NCB>(args, blockIdx.x, wl0, wl1, scw, ad);
+  constexpr bool early = skinny_adapter_early<B, KC, NCB>();
+  __shared__ __attribute__((aligned(16))) __bf16 t_early[early ? adapter_stage_bytes(16) / 2 : 8];
+  skinny_body<B, KC, NCB>(args, blockIdx.x, wl0, wl1, scw, ad, t_early);
 }
 
 // ---------------------------------------------------------------------------
