@@ -235,30 +235,38 @@ __device__ __forceinline__ void adapter_stage(const AdapterArgs& ad, int m, int 
   }
 }
 
-constexpr int kAdapterAhead = 2;
+// The first adapters whose U a wave loads ahead, and how many 32-wide steps of
+// their rank: one column block leaves registers for four adapters of rank 64,
+// four blocks for two of rank 32.
 template <int CB>
 struct AdapterFirst {
-  int adapter[kAdapterAhead];              // -1: none
-  uint64_t match[kAdapterAhead];
-  bf16x8 b[kAdapterAhead][CB];             // U of columns n[c], first 32 of the rank
+  static constexpr int kAhead = CB == 1 ? 4 : 2, kSteps = CB <= 2 ? 2 : 1;
+  int adapter[kAhead];                     // -1: none
+  uint64_t match[kAhead];
+  bf16x8 b[kAhead][kSteps][CB];            // U of columns n[c]
 };
 
 template <int CB>
-__device__ __forceinline__ bf16x8 adapter_u(const AdapterArgs& ad, int adapter, int n_total, int R, int n, int kk) {
-  const __bf16* up = ad.up + ((int64_t)adapter * n_total + n) * R;
-  return keep_or_zero(*reinterpret_cast<const bf16x8*>(up + min(kk, R - 8)), kk < R);
+__device__ __forceinline__ void adapter_u(const AdapterArgs& ad, int adapter, int n_total, int R, const int (&n)[CB],
+                                          int j0, bf16x8 (&b)[CB]) {
+  const int kk = j0 + 8 * (int)((threadIdx.x & 63) >> 4);
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    const __bf16* up = ad.up + ((int64_t)adapter * n_total + n[c]) * R;
+    b[c] = keep_or_zero(*reinterpret_cast<const bf16x8*>(up + min(kk, R - 8)), kk < R);
+  }
 }
 
 // Wave `share` of `shares` takes the distinct adapters share, share + shares, ...
 template <int CB>
 __device__ __forceinline__ void adapter_first(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
                                               int share, int shares, AdapterFirst<CB>& first) {
-  const int lane = threadIdx.x & 63, lq = lane >> 4;
-  const int id[1] = {adapter_of(ad.rows, ad.count, lane, m)};
+  using F = AdapterFirst<CB>;
+  const int id[1] = {adapter_of(ad.rows, ad.count, threadIdx.x & 63, m)};
   AdapterWalk<1> walk(id);
   int d = -1;
 #pragma unroll
-  for (int i = 0; i < kAdapterAhead; ++i) {
+  for (int i = 0; i < F::kAhead; ++i) {
     first.adapter[i] = -1;
     first.match[i] = 0;
     while (walk.next(id)) {
@@ -267,66 +275,68 @@ __device__ __forceinline__ void adapter_first(const AdapterArgs& ad, int m, int 
       first.match[i] = walk.match[0];
       break;
     }
+    if (first.adapter[i] < 0) continue;
 #pragma unroll
-    for (int c = 0; c < CB; ++c)
-      first.b[i][c] = adapter_u<CB>(ad, max(first.adapter[i], 0), n_total, R, n[c], 8 * lq);
+    for (int s = 0; s < F::kSteps; ++s)
+      if (s == 0 || 32 * s < R) adapter_u<CB>(ad, first.adapter[i], n_total, R, n, 32 * s, first.b[i][s]);
   }
 }
 
-// acc += one adapter's branch for the rows `match`, T's parts in LDS.
+// acc += one adapter's step from j0 on for the rows `match`, T's parts in LDS.
 template <int RB, int CB>
-__device__ __forceinline__ void adapter_one(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
-                                            int adapter, uint64_t match, bf16x8 (&b)[CB], const __bf16* lds,
-                                            f32x4 (&acc)[RB][CB]) {
+__device__ __forceinline__ void adapter_step(const AdapterArgs& ad, int m, int R, uint64_t match, int j0,
+                                             const bf16x8 (&b)[CB], const __bf16* lds, f32x4 (&acc)[RB][CB]) {
   const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
-  for (int j0 = 0; j0 < R; j0 += 32) {
-    const int kk = j0 + 8 * lq, kc = min(kk, R - 8);
-    if (j0 > 0) {
+  const int kk = j0 + 8 * lq, kc = min(kk, R - 8);
 #pragma unroll
-      for (int c = 0; c < CB; ++c) b[c] = adapter_u<CB>(ad, adapter, n_total, R, n[c], kk);
+  for (int rb = 0; rb < RB; ++rb) {
+    const uint32_t mask = (uint32_t)(match >> (16 * rb)) & 0xFFFFu;
+    if (mask == 0) continue;
+    f32x4 sum[CB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c) sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < ad.parts; ++p) {
+      const bf16x8 a = keep_or_zero(
+          *reinterpret_cast<const bf16x8*>(lds + ((int64_t)p * m + min(rb * 16 + lr, m - 1)) * R + kc),
+          kk < R && ((mask >> lr) & 1));
+#pragma unroll
+      for (int c = 0; c < CB; ++c) sum[c] = adapter_mfma(a, b[c], sum[c]);
     }
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      const uint32_t mask = (uint32_t)(match >> (16 * rb)) & 0xFFFFu;
-      if (mask == 0) continue;
-      f32x4 sum[CB];
+    for (int i = 0; i < 4; ++i) {
+      const bool mine = (mask >> (4 * lq + i)) & 1;
 #pragma unroll
-      for (int c = 0; c < CB; ++c) sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int p = 0; p < ad.parts; ++p) {
-        const bf16x8 a = keep_or_zero(
-            *reinterpret_cast<const bf16x8*>(lds + ((int64_t)p * m + min(rb * 16 + lr, m - 1)) * R + kc),
-            kk < R && ((mask >> lr) & 1));
-#pragma unroll
-        for (int c = 0; c < CB; ++c) sum[c] = adapter_mfma(a, b[c], sum[c]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool mine = (mask >> (4 * lq + i)) & 1;
-#pragma unroll
-        for (int c = 0; c < CB; ++c) acc[rb][c][i] += mine ? sum[c][i] : 0.0f;
-      }
+      for (int c = 0; c < CB; ++c) acc[rb][c][i] += mine ? sum[c][i] : 0.0f;
     }
   }
 }
 
 template <int RB, int CB>
 __device__ __forceinline__ void adapter_rows16(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
-                                               int share, int shares, AdapterFirst<CB>& first, const __bf16* lds,
-                                               f32x4 (&acc)[RB][CB]) {
-  const int lane = threadIdx.x & 63, lq = lane >> 4;
+                                               int share, int shares, const AdapterFirst<CB>& first,
+                                               const __bf16* lds, f32x4 (&acc)[RB][CB]) {
+  using F = AdapterFirst<CB>;
 #pragma unroll
-  for (int i = 0; i < kAdapterAhead; ++i)
-    if (first.adapter[i] >= 0)
-      adapter_one<RB, CB>(ad, m, n_total, R, n, first.adapter[i], first.match[i], first.b[i], lds, acc);
-  if (first.adapter[kAdapterAhead - 1] < 0) return;
-  const int id[1] = {adapter_of(ad.rows, ad.count, lane, m)};
+  for (int i = 0; i < F::kAhead; ++i) {
+    if (first.adapter[i] < 0) return;
+#pragma unroll
+    for (int s = 0; s < F::kSteps; ++s)
+      if (s == 0 || 32 * s < R) adapter_step<RB, CB>(ad, m, R, first.match[i], 32 * s, first.b[i][s], lds, acc);
+    for (int j0 = 32 * F::kSteps; j0 < R; j0 += 32) {
+      bf16x8 b[CB];
+      adapter_u<CB>(ad, first.adapter[i], n_total, R, n, j0, b);
+      adapter_step<RB, CB>(ad, m, R, first.match[i], j0, b, lds, acc);
+    }
+  }
+  const int id[1] = {adapter_of(ad.rows, ad.count, threadIdx.x & 63, m)};
   AdapterWalk<1> walk(id);
   for (int d = 0; walk.next(id); ++d) {
-    if (d % shares != share || d < shares * kAdapterAhead) continue;
-    bf16x8 b[CB];
-#pragma unroll
-    for (int c = 0; c < CB; ++c) b[c] = adapter_u<CB>(ad, walk.adapter, n_total, R, n[c], 8 * lq);
-    adapter_one<RB, CB>(ad, m, n_total, R, n, walk.adapter, walk.match[0], b, lds, acc);
+    if (d % shares != share || d < shares * F::kAhead) continue;
+    for (int j0 = 0; j0 < R; j0 += 32) {
+      bf16x8 b[CB];
+      adapter_u<CB>(ad, walk.adapter, n_total, R, n, j0, b);
+      adapter_step<RB, CB>(ad, m, R, walk.match[0], j0, b, lds, acc);
+    }
   }
 }
 
@@ -358,9 +368,10 @@ struct AdapterDown {
   int run;                  // row blocks in a row before the next z
 };
 
-// Waves per workgroup for a step of RR + RBLK row blocks (two stages of 2 KB
-// per row block and wave, at most 128 KB).
-constexpr int adapter_down_waves(int rr, int rblk) { return rr + rblk <= 2 ? 16 : (rr + rblk <= 4 ? 8 : 4); }
+// Waves per workgroup: at most 8, and no more than leave room for a second
+// workgroup on the compute unit (two stages of 2 KB per row block and wave;
+// 16 waves with one row block each took 13.4 us where 8 take 11.2).
+constexpr int adapter_down_waves(int rr, int rblk) { return 20 / (rr + rblk) < 8 ? 20 / (rr + rblk) : 8; }
 
 template <int RBLK, int RR, bool PARTS>
 __global__ __launch_bounds__(64 * adapter_down_waves(RR, RBLK)) void adapter_down_kernel(AdapterDown a) {
