@@ -5,7 +5,7 @@
 //                         `chunks` parts of K, which the product adds up in
 //                         order; for more rows the bf16 parts of T
 //   adapter_tile          the branch of a 256-row tile
-//   adapter_stage, adapter_first, adapter_rows16
+//   AdapterStage, adapter_first, adapter_rows16
 //                         the branch of at most 64 rows
 //
 // A block of rows may mix adapters.  Every wave walks the distinct adapters of
@@ -197,24 +197,30 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n
 
 // ---------------------------------------------------------------------------
 // At most 64 rows.  The workgroup adds T's chunks up into LDS once
-// (adapter_stage) as bf16 parts; its K-split waves share out the distinct
+// (AdapterStage) as bf16 parts; its K-split waves share out the distinct
 // adapters, and the first two adapters' U of each wave are loaded before the
 // K loop (adapter_first) and used behind it.
 // ---------------------------------------------------------------------------
 constexpr size_t adapter_stage_bytes(int rows) { return (size_t)kAdapterMaxParts * rows * 128 * 2; }
 
-__device__ __forceinline__ void adapter_stage(const AdapterArgs& ad, int m, int R, __bf16* lds, int tid, int n) {
-  const int per_row = R / 8;
-  for (int i = tid; i < m * per_row; i += n) {
-    const float* p = ad.t + (int64_t)i * 8;                   // T is dense: row i / per_row, column 8 (i % per_row)
-    f32x4 lo[kAdapterMaxChunks], hi[kAdapterMaxChunks];
+// Loads complete in the order they are issued, so what a wave needs first it
+// has to load first: the row ids and the first T values (begin) go out ahead
+// of the kernel's own loads, and U, which is needed last, behind them.
+struct AdapterStage {
+  int id;                                                     // of row `lane`
+  f32x4 lo[kAdapterMaxChunks], hi[kAdapterMaxChunks];
+
+  __device__ __forceinline__ void load(const AdapterArgs& ad, int m, int R, int i) {
+    const float* p = ad.t + (int64_t)i * 8;                   // T is dense: row i / (R / 8), column 8 (i % (R / 8))
 #pragma unroll
     for (int c = 0; c < kAdapterMaxChunks; ++c) {
-      // past the last chunk: the last one again, not added
-      const float* pc = p + (int64_t)min(c, ad.chunks - 1) * m * R;
+      if (c >= ad.chunks) break;
+      const float* pc = p + (int64_t)c * m * R;
       lo[c] = *reinterpret_cast<const f32x4*>(pc);
       hi[c] = *reinterpret_cast<const f32x4*>(pc + 4);
     }
+  }
+  __device__ __forceinline__ void write(const AdapterArgs& ad, int m, int R, int i, __bf16* lds) {
     float t[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -233,7 +239,19 @@ __device__ __forceinline__ void adapter_stage(const AdapterArgs& ad, int m, int 
     for (int part = 0; part < ad.parts; ++part)
       *reinterpret_cast<u32x4*>(lds + ((int64_t)part * m * R + i * 8)) = take_part(t);
   }
-}
+  __device__ __forceinline__ void begin(const AdapterArgs& ad, int m, int R, bool early, int tid) {
+    id = adapter_of(ad.rows, ad.count, threadIdx.x & 63, m);
+    if (early) load(ad, m, R, min(tid, m * (R / 8) - 1));
+  }
+  // T's parts to lds; started: begin loaded the thread's first values
+  __device__ __forceinline__ void finish(const AdapterArgs& ad, int m, int R, bool started, __bf16* lds, int tid,
+                                         int n) {
+    for (int i = tid; i < m * (R / 8); i += n) {
+      if (!started || i != tid) load(ad, m, R, i);
+      write(ad, m, R, i, lds);
+    }
+  }
+};
 
 // The first adapters whose U a wave loads ahead, and how many 32-wide steps of
 // their rank: one column block leaves registers for four adapters of rank 64,
@@ -259,10 +277,10 @@ __device__ __forceinline__ void adapter_u(const AdapterArgs& ad, int adapter, in
 
 // Wave `share` of `shares` takes the distinct adapters share, share + shares, ...
 template <int CB>
-__device__ __forceinline__ void adapter_first(const AdapterArgs& ad, int m, int n_total, int R, const int (&n)[CB],
-                                              int share, int shares, AdapterFirst<CB>& first) {
+__device__ __forceinline__ void adapter_first(const AdapterArgs& ad, int row_id, int n_total, int R,
+                                              const int (&n)[CB], int share, int shares, AdapterFirst<CB>& first) {
   using F = AdapterFirst<CB>;
-  const int id[1] = {adapter_of(ad.rows, ad.count, threadIdx.x & 63, m)};
+  const int id[1] = {row_id};
   AdapterWalk<1> walk(id);
   int d = -1;
 #pragma unroll

@@ -1258,6 +1258,9 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
     }
     if (j < cnt) compute(xslot(integral_constant<int, U % S>{}), U % S);
   };
+  [[maybe_unused]] AdapterStage stage;
+  constexpr bool early = small_adapter_early<RB, NC, NK>();
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) stage.begin(ad, args.m, args.r, early, threadIdx.x);
   // prologue: steps 0..D-1
   [&]<int... J>(std::integer_sequence<int, J...>) {
     ((load_x(J, J), load_w(J, J)), ...);
@@ -1265,10 +1268,11 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
   // the K splits share out the rows' distinct adapters
   [[maybe_unused]] const int ad_col[1] = {n};
   [[maybe_unused]] AdapterFirst<1> first;
-  if constexpr (std::is_same_v<Ad, AdapterArgs>)
-    adapter_first<1>(ad, args.m, args.n, args.r, ad_col, part * NK + h, sp.parts * NK, first);
-  if constexpr (std::is_same_v<Ad, AdapterArgs> && small_adapter_early<RB, NC, NK>())
-    adapter_stage(ad, args.m, args.r, t_early, threadIdx.x, 64 * NC * NK);     // (barriers follow)
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+    if constexpr (early)
+      stage.finish(ad, args.m, args.r, true, t_early, threadIdx.x, 64 * NC * NK);     // (barriers follow)
+    adapter_first<1>(ad, stage.id, args.n, args.r, ad_col, part * NK + h, sp.parts * NK, first);
+  }
   // main loop: whole blocks of S steps (every ring index a constant)
   const int full = steps / S * S;
   for (int j0 = 0; j0 < full; j0 += S) {
@@ -1291,11 +1295,11 @@ __device__ __forceinline__ void small_body(const GemmArgs& args, int wg, SmallLd
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
     __bf16* t_lds = t_early;
-    if constexpr (!small_adapter_early<RB, NC, NK>()) {
+    if constexpr (!early) {
       // into the X ring, which every wave is done with
       static_assert(S * NK * XSLOT >= adapter_stage_bytes(16 * RB), "T's parts fit the X ring");
       t_lds = reinterpret_cast<__bf16*>(&L.xs0[0][0]);
-      adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NC * NK);
+      stage.finish(ad, args.m, args.r, false, t_lds, threadIdx.x, 64 * NC * NK);
       __syncthreads();
     }
     f32x4 br[RB][1];
@@ -1593,6 +1597,9 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
   // chunk loop is unrolled by two so that every buffer index is static.
   constexpr int CU = (NCB & 1) ? 2 : 1;
   using std::integral_constant;
+  [[maybe_unused]] AdapterStage stage;
+  constexpr bool early = skinny_adapter_early<B, KC, NCB>();
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) stage.begin(ad, args.m, args.r, early, threadIdx.x);
   uint32_t off_cur[NDMA], off_next[NDMA];
   chunk_offsets(0, off_cur);
   load_w(integral_constant<int, 0>{}, 0, off_cur);
@@ -1610,9 +1617,19 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
     if (c < nch) compute(integral_constant<int, cur>{}, CB, c);
     __builtin_amdgcn_sched_barrier(0);
   };
+  // the eight K splits share out the rows' distinct adapters
+  [[maybe_unused]] int ad_col[NCB];
+  [[maybe_unused]] AdapterFirst<NCB> first;
+  if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+#pragma unroll
+    for (int cb = 0; cb < NCB; ++cb) ad_col[cb] = min(n0 + cb * 16 + lr, args.n - 1);
+  }
   auto chunk_body = [&]<int U>(integral_constant<int, U> u, int c) __attribute__((always_inline)) {
     load_scales(c);
     load_x(c);
+    if constexpr (std::is_same_v<Ad, AdapterArgs>) {
+      if (c == 0) adapter_first<NCB>(ad, stage.id, args.n, args.r, ad_col, wave, NW, first);
+    }
     __builtin_amdgcn_sched_barrier(0);
     [&]<int... CB>(std::integer_sequence<int, CB...>) __attribute__((always_inline)) {
       (block(u, integral_constant<int, CB>{}, c), ...);
@@ -1620,14 +1637,10 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
 #pragma unroll
     for (int d = 0; d < NDMA; ++d) off_cur[d] = off_next[d];
   };
-  // the eight K splits share out the rows' distinct adapters
-  [[maybe_unused]] int ad_col[NCB];
-  [[maybe_unused]] AdapterFirst<NCB> first;
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-#pragma unroll
-    for (int cb = 0; cb < NCB; ++cb) ad_col[cb] = min(n0 + cb * 16 + lr, args.n - 1);
-    adapter_first<NCB>(ad, args.m, args.n, args.r, ad_col, wave, NW, first);
-    if constexpr (skinny_adapter_early<B, KC, NCB>()) adapter_stage(ad, args.m, args.r, t_early, threadIdx.x, 64 * NW);
+    if constexpr (early) stage.finish(ad, args.m, args.r, true, t_early, threadIdx.x, 64 * NW);
+    // a wave without groups has no chunk to load U behind
+    if (nch == 0) adapter_first<NCB>(ad, stage.id, args.n, args.r, ad_col, wave, NW, first);
   }
   for (int c0 = 0; c0 < nch; c0 += CU) {
     [&]<int... U>(std::integer_sequence<int, U...>) __attribute__((always_inline)) {
@@ -1640,13 +1653,13 @@ __device__ __forceinline__ void skinny_body(const GemmArgs& args, int wg, uint8_
 #pragma unroll
     for (int cb = 0; cb < NCB; ++cb) br[0][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
     __bf16* t_lds = t_early;
-    if constexpr (!skinny_adapter_early<B, KC, NCB>()) {
+    if constexpr (!early) {
       // into the first weight buffer, once every wave is done with it
       static_assert(SkinnyLds<B, KC, NCB>::W0 >= adapter_stage_bytes(16), "T's parts fit the first weight buffer");
       __builtin_amdgcn_s_waitcnt(0);
       __syncthreads();
       t_lds = reinterpret_cast<__bf16*>(wl0);
-      adapter_stage(ad, args.m, args.r, t_lds, threadIdx.x, 64 * NW);
+      stage.finish(ad, args.m, args.r, false, t_lds, threadIdx.x, 64 * NW);
     }
     __syncthreads();
     adapter_rows16<1, NCB>(ad, args.m, args.n, args.r, ad_col, wave, NW, first, t_lds, br);
