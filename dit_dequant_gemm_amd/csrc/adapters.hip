@@ -98,10 +98,11 @@ hipError_t launch_adapter_down(const AdapterDown& d, hipStream_t stream) {
   // at most 64 rows: every distinct adapter of a row block and every 16 of
   // the rank in a workgroup of its own
   if (d.m <= kAdapterFewRows) return launch_down<1, 1, false>(d, std::min(d.count, 16), stream);
-  // a block's second adapter goes to a second workgroup: blocks with a
-  // request's end inside would otherwise take twice as long as the others
-  const int z = std::min(d.count, 2);
+  // a block's adapters go to different workgroups, two at least (blocks with a
+  // request's end inside would otherwise take twice as long as the others),
+  // more while that leaves at most four workgroups per compute unit
   const int blocks = (d.m + 15) / 16;
+  const int z = std::min(d.count, std::max(2, std::min(16, 1024 / blocks)));
   if (blocks < 128) return launch_down<1, 1, true>(d, z, stream);
   // D is read once per workgroup: several row blocks to one while every
   // compute unit gets a workgroup

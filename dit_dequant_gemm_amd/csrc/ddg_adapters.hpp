@@ -4,7 +4,8 @@
 //   adapter_down_kernel   T (times s_a): for at most 64 rows float32 sums over
 //                         `chunks` parts of K, which the product adds up in
 //                         order; for more rows the bf16 parts of T
-//   adapter_tile          the branch of a 256-row tile
+//   adapter_tile, adapter_mixed
+//                         the branch of a 256-row tile
 //   AdapterStage, adapter_first, adapter_rows16
 //                         the branch of at most 64 rows
 //
@@ -78,6 +79,18 @@ __device__ __forceinline__ f32x16 adapter_mfma(bf16x8 a, bf16x8 b, f32x16 c) {
 }
 __device__ __forceinline__ f32x4 adapter_mfma(bf16x8 a, bf16x8 b, f32x4 c) { return mfma16x16x32(a, b, c); }
 
+// An infinity in accumulator c for the rows `mine` in the columns whose U is
+// broken (lanes, any k part): the largest bf16 squared; zeros elsewhere.
+template <int ROWS, typename Acc>
+__device__ __forceinline__ Acc adapter_blow(uint64_t broken, bool mine, Acc c) {
+  const bf16x8 big = __builtin_bit_cast(bf16x8, u32x4{0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu});
+  const int l = threadIdx.x & (ROWS - 1);
+  bool mark = false;
+#pragma unroll
+  for (int i = 0; i < 64 / ROWS; ++i) mark |= (broken >> (l + i * ROWS)) & 1;
+  return adapter_mfma(keep_or_zero(big, mine), keep_or_zero(big, mark), c);
+}
+
 // Distinct adapters of up to 64 W rows (id[j]: row 64 j + lane), one at a time.
 template <int W>
 struct AdapterWalk {
@@ -86,6 +99,12 @@ struct AdapterWalk {
   __device__ __forceinline__ explicit AdapterWalk(const int (&id)[W]) {
 #pragma unroll
     for (int j = 0; j < W; ++j) pending[j] = __ballot(id[j] >= 0);
+  }
+  __device__ __forceinline__ bool more() const {
+    uint64_t any = 0;
+#pragma unroll
+    for (int j = 0; j < W; ++j) any |= pending[j];
+    return any != 0;
   }
   __device__ __forceinline__ bool next(const int (&id)[W]) {
     bool found = false;
@@ -107,91 +126,190 @@ struct AdapterWalk {
 };
 
 // ---------------------------------------------------------------------------
-// 256-row tiles: the branch goes into the accumulators before the K loop.  The
-// tile's first adapter (FIRST) is straight-line code behind the first group's
-// loads, where its latencies overlap theirs.  The other adapters, which only
-// tiles that mix requests have, are a loop ahead of them: a loop over the
-// adapters behind those loads made the compiler spill around the K loop and
-// cost every tile 10 us, also without any adapter (32760 x 15360 x 5120: 4018
-// us for the product alone, 4311 with rows that name none; now 4150 and 4175).
-//
-// T and U are read through buffer resources (one offset register instead of a
-// 64-bit address per row block; rows past M and columns past N read as zeros),
-// and the rows of an adapter are lane masks in scalar registers.
+// 256-row tiles: the branch goes into the accumulators before the K loop.  A
+// tile of one adapter (adapter_tile) is straight-line code behind the first
+// group's loads, where its latencies overlap theirs.  A tile that mixes
+// adapters (adapter_mixed) is done ahead of those loads, while the LDS is
+// free: a loop over adapters behind them made the compiler spill around the K
+// loop and cost every tile 10 us, also without any adapter (32760 x 15360 x
+// 5120: 4018 us for the product alone, 4311 with rows that name none; now 4150
+// and 4175).
 //
 // ROWS x (256 / ROWS) row blocks, CB column blocks of ROWS from column col0
 // on; lane (row or column l, k part q) of the operands.
 // ---------------------------------------------------------------------------
-template <int ROWS, int CB, bool FIRST, typename Acc>
+template <int ROWS>
+struct TileLanes {
+  static constexpr int KS = ROWS == 32 ? 16 : 32;             // rank of a matrix instruction
+  int l, q;
+  __device__ __forceinline__ TileLanes() {
+    const int lane = threadIdx.x & 63;
+    l = lane & (ROWS - 1);
+    q = lane / ROWS;
+  }
+  // rows `bits` of a row block, for every k part's lanes
+  static __device__ __forceinline__ bool mine(uint32_t bits) {
+    return __builtin_amdgcn_inverse_ballot_w64(ROWS == 32 ? bits * 0x100000001ull : (bits & 0xFFFFu) * 0x1000100010001ull);
+  }
+};
+
+template <int ROWS, int CB, typename Acc>
 __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n_total, int R, int m0, int col0,
                                              Acc (&acc)[256 / ROWS][CB]) {
-  constexpr int RB = 256 / ROWS, KS = ROWS == 32 ? 16 : 32;
+  constexpr int RB = 256 / ROWS, KS = TileLanes<ROWS>::KS;
   constexpr int BATCH = 8;                                     // T operands in flight
-  const int lane = threadIdx.x & 63, l = lane & (ROWS - 1), q = lane / ROWS;
+  const TileLanes<ROWS> tl;
   int id[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + lane, m);
+  for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + (threadIdx.x & 63), m);
+  AdapterWalk<4> walk(id);
+  if (!walk.next(id) || walk.more()) return;
+  // T and U through buffer resources: one offset register instead of a 64-bit
+  // address per row block; rows past M and columns past N read as zeros
   const uint32_t row_bytes = (uint32_t)R * 2;
   const uint32_t t_bytes = (uint32_t)min(256, m - m0) * row_bytes;
   const uint32_t u_bytes = (uint32_t)max(0, min(CB * ROWS, n_total - col0)) * row_bytes;
-  const uint32_t lane_off = (uint32_t)l * row_bytes;
-  AdapterWalk<4> walk(id);
-  if (!walk.next(id)) return;                                  // to the first adapter
-  for (bool more = FIRST || walk.next(id); more; more = !FIRST && walk.next(id)) {
-    const rsrc_t ru = make_rsrc(ad.up + ((int64_t)walk.adapter * n_total + col0) * R, u_bytes);
-    const bool whole = (walk.match[0] & walk.match[1] & walk.match[2] & walk.match[3]) == ~0ull;
-    uint64_t broken[CB] = {};                                  // lanes whose U holds an infinity or a NaN
-    // row block rb's rows of this adapter, for every k part's lanes
-    auto mine = [&](int rb) -> bool {
-      const uint64_t w = walk.match[rb * ROWS / 64] >> (rb * ROWS % 64);
-      return __builtin_amdgcn_inverse_ballot_w64(ROWS == 32 ? (w & 0xFFFFFFFFull) * 0x100000001ull
-                                                            : (w & 0xFFFFull) * 0x1000100010001ull);
-    };
-    for (int j0 = 0; j0 < R; j0 += KS) {
-      const int kk = j0 + 8 * q;
-      // a k part past the rank: past the resource, zeros
-      const uint32_t off = kk < R ? lane_off + (uint32_t)kk * 2 : 0x80000000u;
-      bf16x8 b[CB];
-#pragma unroll
-      for (int c = 0; c < CB; ++c) {
-        b[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, off + c * ROWS * row_bytes, 0, 0));
-        if (!whole) {
-          const bool bad = nonfinite(b[c]);
-          broken[c] |= __ballot(bad);
-          b[c] = keep_or_zero(b[c], !bad);
-        }
-      }
-      for (int p = 0; p < ad.parts; ++p) {
-        const rsrc_t rt = make_rsrc(ad.t16 + ((int64_t)p * m + m0) * R, t_bytes);
-#pragma unroll
-        for (int r0 = 0; r0 < RB; r0 += BATCH) {
-          bf16x8 a[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i)
-            a[i] = __builtin_bit_cast(
-                bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rt, off + (r0 + i) * ROWS * row_bytes, 0, 0));
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            a[i] = keep_or_zero(a[i], mine(r0 + i));
-#pragma unroll
-            for (int c = 0; c < CB; ++c) acc[r0 + i][c] = adapter_mfma(a[i], b[c], acc[r0 + i][c]);
-          }
-        }
-      }
-    }
-    // its rows' outputs in the columns of an infinity or a NaN: the largest
-    // bf16 squared, an infinity in the accumulator (zeros elsewhere)
+  const rsrc_t ru = make_rsrc(ad.up + ((int64_t)walk.adapter * n_total + col0) * R, u_bytes);
+  // rows without an adapter: their T was not written, and U may hold
+  // infinities, whose product with zero is a NaN
+  const bool whole = (walk.match[0] & walk.match[1] & walk.match[2] & walk.match[3]) == ~0ull;
+  uint64_t broken[CB] = {};                                    // lanes whose U holds an infinity or a NaN
+  auto mine = [&](int rb) { return tl.mine((uint32_t)(walk.match[rb * ROWS / 64] >> (rb * ROWS % 64))); };
+  for (int j0 = 0; j0 < R; j0 += KS) {
+    const int kk = j0 + 8 * tl.q;
+    // a k part past the rank: past the resource, zeros
+    const uint32_t off = kk < R ? (uint32_t)tl.l * row_bytes + (uint32_t)kk * 2 : 0x80000000u;
+    bf16x8 b[CB];
 #pragma unroll
     for (int c = 0; c < CB; ++c) {
-      if (broken[c] == 0) continue;
-      const bf16x8 big = __builtin_bit_cast(bf16x8, u32x4{0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu});
-      bool mark = false;
-#pragma unroll
-      for (int i = 0; i < 64 / ROWS; ++i) mark |= (broken[c] >> (l + i * ROWS)) & 1;
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-        acc[rb][c] = adapter_mfma(keep_or_zero(big, mine(rb)), keep_or_zero(big, mark), acc[rb][c]);
+      b[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, off + c * ROWS * row_bytes, 0, 0));
+      if (!whole) {
+        const bool bad = nonfinite(b[c]);
+        broken[c] |= __ballot(bad);
+        b[c] = keep_or_zero(b[c], !bad);
+      }
     }
+    for (int p = 0; p < ad.parts; ++p) {
+      const rsrc_t rt = make_rsrc(ad.t16 + ((int64_t)p * m + m0) * R, t_bytes);
+#pragma unroll
+      for (int r0 = 0; r0 < RB; r0 += BATCH) {
+        bf16x8 a[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          a[i] = __builtin_bit_cast(
+              bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rt, off + (r0 + i) * ROWS * row_bytes, 0, 0));
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          a[i] = keep_or_zero(a[i], mine(r0 + i));
+#pragma unroll
+          for (int c = 0; c < CB; ++c) acc[r0 + i][c] = adapter_mfma(a[i], b[c], acc[r0 + i][c]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CB; ++c)
+    if (broken[c] != 0) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) acc[rb][c] = adapter_blow<ROWS>(broken[c], mine(rb), acc[rb][c]);
+    }
+}
+
+// A tile of several adapters, by the whole workgroup of n lanes.  T comes
+// through LDS, one rank step at a time (every adapter's turn reads it again),
+// and so does the list of the tile's adapters with their row masks, which the
+// first wave writes: with both at hand, U's loads of the next adapters are in
+// flight while one is multiplied, and row blocks without its rows are
+// skipped.  On return no wave needs the LDS.
+constexpr int kAdapterDepth = 4;                               // adapters whose U is in flight
+constexpr int kAdapterListAt = 3 * 256 * 64;                   // behind T's parts (32 ranks at most)
+constexpr int kAdapterEntry = 5;                               // 64-bit words: row masks, adapter
+
+template <int ROWS, int CB, typename Acc>
+__device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int n_total, int R, int m0, int col0,
+                                              Acc (&acc)[256 / ROWS][CB], uint8_t* lds, int n) {
+  constexpr int RB = 256 / ROWS, KS = TileLanes<ROWS>::KS;
+  const TileLanes<ROWS> tl;
+  const int tid = threadIdx.x;
+  int id[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + (tid & 63), m);
+  AdapterWalk<4> walk(id);
+  if (!walk.next(id) || !walk.more()) return;                  // the same in every wave
+  uint64_t* list = reinterpret_cast<uint64_t*>(lds + kAdapterListAt);
+  if (tid < 64) {
+    int count = 0;
+    do {
+      if (tid == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) list[1 + count * kAdapterEntry + j] = walk.match[j];
+        list[1 + count * kAdapterEntry + 4] = (uint64_t)walk.adapter;
+      }
+      ++count;
+    } while (walk.next(id));
+    if (tid == 0) list[0] = (uint64_t)count;
+  }
+  const uint32_t row_bytes = (uint32_t)R * 2;
+  const uint32_t u_bytes = (uint32_t)max(0, min(CB * ROWS, n_total - col0)) * row_bytes;
+  for (int j0 = 0; j0 < R; j0 += KS) {
+    // T's parts of this rank step: [part][row][KS], zeros past the rank and past M
+    constexpr int PIECES = KS / 8;
+    for (int i = tid; i < ad.parts * 256 * PIECES; i += n) {
+      const int piece = i % PIECES, row = i / PIECES % 256, p = i / (PIECES * 256);
+      const int kk = j0 + 8 * piece;
+      const bf16x8 v = *reinterpret_cast<const bf16x8*>(ad.t16 + ((int64_t)p * m + min(m0 + row, m - 1)) * R +
+                                                        min(kk, R - 8));
+      *reinterpret_cast<bf16x8*>(lds + i * 16) = keep_or_zero(v, kk < R && m0 + row < m);
+    }
+    __syncthreads();
+    const int count = __builtin_amdgcn_readfirstlane((int)list[0]);
+    const int kk = j0 + 8 * tl.q;
+    const uint32_t off = kk < R ? (uint32_t)tl.l * row_bytes + (uint32_t)kk * 2 : 0x80000000u;
+    bf16x8 b[kAdapterDepth][CB];
+    auto load_u = [&](int i, bf16x8 (&u)[CB]) __attribute__((always_inline)) {
+      const int adapter = __builtin_amdgcn_readfirstlane((int)list[1 + min(i, count - 1) * kAdapterEntry + 4]);
+      const rsrc_t ru = make_rsrc(ad.up + ((int64_t)adapter * n_total + col0) * R, u_bytes);
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+        u[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, off + c * ROWS * row_bytes, 0, 0));
+    };
+#pragma unroll
+    for (int u = 0; u < kAdapterDepth; ++u) load_u(u, b[u]);
+    for (int i0 = 0; i0 < count; i0 += kAdapterDepth) {
+#pragma unroll
+      for (int u = 0; u < kAdapterDepth; ++u) {
+        if (i0 + u >= count) break;
+        uint32_t bits[RB];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          const uint32_t* words = reinterpret_cast<const uint32_t*>(list + 1 + (i0 + u) * kAdapterEntry);
+          const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)words[rb * ROWS / 32]);
+          bits[rb] = ROWS == 32 ? w : (w >> (rb * ROWS % 32)) & 0xFFFFu;
+        }
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+          const bool bad = nonfinite(b[u][c]);
+          const uint64_t broken = __ballot(bad);
+          if (broken != 0) {
+            b[u][c] = keep_or_zero(b[u][c], !bad);
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) acc[rb][c] = adapter_blow<ROWS>(broken, tl.mine(bits[rb]), acc[rb][c]);
+          }
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+          if (bits[rb] == 0) continue;
+          for (int p = 0; p < ad.parts; ++p) {
+            const bf16x8 t = *reinterpret_cast<const bf16x8*>(lds + ((p * 256 + rb * ROWS + tl.l) * PIECES + tl.q) * 16);
+            const bf16x8 a = keep_or_zero(t, tl.mine(bits[rb]));
+#pragma unroll
+            for (int c = 0; c < CB; ++c) acc[rb][c] = adapter_mfma(a, b[u][c], acc[rb][c]);
+          }
+        }
+        load_u(i0 + u + kAdapterDepth, b[u]);
+      }
+    }
+    __syncthreads();                                           // T's LDS is free
   }
 }
 

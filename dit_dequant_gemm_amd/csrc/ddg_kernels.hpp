@@ -281,7 +281,7 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
   const rsrc_t rs = make_rsrc(args.scales + (int64_t)nw0 * G, (uint32_t)n_valid * G * 4);
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    if (lowrank) adapter_tile<32, 1, false>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc));
+    if (lowrank) adapter_mixed<32, 1>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc), lds, 512);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -356,7 +356,7 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
   // their latencies overlap (32760 x 5120 x 5120, r = 32: 1558 -> 1504 us for
   // the fused call); it still adds into acc before the K loop
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    if (lowrank) adapter_tile<32, 1, true>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc));
+    if (lowrank) adapter_tile<32, 1>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc));
   } else if (lowrank && args.t != nullptr) {
     // acc = T * lora_up^T over the rank dimension, 16 at a time (zero-padded).
     const int R = args.r;
@@ -580,7 +580,7 @@ __device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, 
     for (int c = 0; c < CB; ++c) acc[rb][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    adapter_tile<16, CB, false>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc);
+    adapter_mixed<16, CB>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc, lds, 256);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -628,7 +628,7 @@ __device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, 
   // the low-rank branch behind the first group's loads, as in K2
   // (4096 x 3072 x 3072, r = 32: 87.6 -> 84.3 us for the fused call)
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    adapter_tile<16, CB, true>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc);
+    adapter_tile<16, CB>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc);
   } else if (args.t != nullptr) {
     // acc = T * lora_up^T over the rank dimension, 32 at a time (zero-padded).
     const int R = args.r;

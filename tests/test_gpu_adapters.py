@@ -102,6 +102,22 @@ def test_shapes_and_mixes(gpu_lib, m, n, k, bits, kind):
         _check(y, _reference(gpu_lib, x, qw, pool, rows), k, r, (kind, a, r))
 
 
+@pytest.mark.parametrize("m,n,k", [(64, 272, 384), (65, 272, 384), (256, 1040, 640), (300, 528, 1536), (511, 5136, 256),
+                                   (4100, 3088, 256)])
+def test_every_row_its_own_adapter(gpu_lib, m, n, k):
+    """As many adapters as rows, in any order and with a few rows of none: 256
+    of them in a tile, 16 in a row block of the pre-pass."""
+    for r, dt in [(16, BF), (8, F32), (40, F32)]:
+        _case(f"every row its own adapter {m}x{n}x{k} rank={r} {dt}")
+        a = min(m, 700)
+        x, qw, pool = _setup(gpu_lib, m + r, m, n, k, 4, a, r)
+        rows = _rows("each", m, a, m)
+        rows[::37] = -1
+        y = gpu_lib.adapter_gemm(x, qw, pool, rows, out_dtype=dt)
+        _check(y, _reference(gpu_lib, x, qw, pool, rows), k, r, (m, r))
+        assert torch.equal(y, gpu_lib.adapter_gemm(x, qw, pool, rows, out_dtype=dt))
+
+
 @pytest.mark.parametrize("r", [8, 16, 24, 32, 48, 56, 64, 72, 80, 96, 104, 112, 120, 128])
 @pytest.mark.parametrize("m", [5, 70, 2100])
 def test_ranks(gpu_lib, m, r):
