@@ -220,14 +220,16 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n
 // and so does the list of the tile's adapters with their row masks, which the
 // first wave writes: with both at hand, U's loads of the next adapters are in
 // flight while one is multiplied, and row blocks without its rows are
-// skipped.  On return no wave needs the LDS.
+// skipped.  Of the list, entries share, share + shares, ... (workgroups that
+// split K share out the adapters too).  On return no wave needs the LDS.
 constexpr int kAdapterDepth = 4;                               // adapters whose U is in flight
 constexpr int kAdapterListAt = 3 * 256 * 64;                   // behind T's parts (32 ranks at most)
 constexpr int kAdapterEntry = 5;                               // 64-bit words: row masks, adapter
 
 template <int ROWS, int CB, typename Acc>
 __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int n_total, int R, int m0, int col0,
-                                              Acc (&acc)[256 / ROWS][CB], uint8_t* lds, int n) {
+                                              Acc (&acc)[256 / ROWS][CB], uint8_t* lds, int n, int share = 0,
+                                              int shares = 1) {
   constexpr int RB = 256 / ROWS, KS = TileLanes<ROWS>::KS;
   const TileLanes<ROWS> tl;
   const int tid = threadIdx.x;
@@ -262,19 +264,22 @@ __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int 
       *reinterpret_cast<bf16x8*>(lds + i * 16) = keep_or_zero(v, kk < R && m0 + row < m);
     }
     __syncthreads();
-    const int count = __builtin_amdgcn_readfirstlane((int)list[0]);
+    const int count = (__builtin_amdgcn_readfirstlane((int)list[0]) - share + shares - 1) / shares;     // this share's
     const int kk = j0 + 8 * tl.q;
     const uint32_t off = kk < R ? (uint32_t)tl.l * row_bytes + (uint32_t)kk * 2 : 0x80000000u;
     bf16x8 b[kAdapterDepth][CB];
     auto load_u = [&](int i, bf16x8 (&u)[CB]) __attribute__((always_inline)) {
-      const int adapter = __builtin_amdgcn_readfirstlane((int)list[1 + min(i, count - 1) * kAdapterEntry + 4]);
+      const int at = 1 + (share + min(i, count - 1) * shares) * kAdapterEntry;
+      const int adapter = __builtin_amdgcn_readfirstlane((int)list[at + 4]);
       const rsrc_t ru = make_rsrc(ad.up + ((int64_t)adapter * n_total + col0) * R, u_bytes);
 #pragma unroll
       for (int c = 0; c < CB; ++c)
         u[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, off + c * ROWS * row_bytes, 0, 0));
     };
+    if (count > 0) {
 #pragma unroll
-    for (int u = 0; u < kAdapterDepth; ++u) load_u(u, b[u]);
+      for (int u = 0; u < kAdapterDepth; ++u) load_u(u, b[u]);
+    }
     for (int i0 = 0; i0 < count; i0 += kAdapterDepth) {
 #pragma unroll
       for (int u = 0; u < kAdapterDepth; ++u) {
@@ -282,7 +287,8 @@ __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int 
         uint32_t bits[RB];
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-          const uint32_t* words = reinterpret_cast<const uint32_t*>(list + 1 + (i0 + u) * kAdapterEntry);
+          const uint32_t* words =
+              reinterpret_cast<const uint32_t*>(list + 1 + (share + (i0 + u) * shares) * kAdapterEntry);
           const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)words[rb * ROWS / 32]);
           bits[rb] = ROWS == 32 ? w : (w >> (rb * ROWS % 32)) & 0xFFFFu;
         }

@@ -253,11 +253,12 @@ __device__ __forceinline__ f32x16 (&tile_blocks(f32x16 (&acc)[kBM / 32]))[kBM / 
 // T * lora_up^T of the tile is added first.  `lds` is the workgroup's 128 KB
 // LDS block; on return the last group's LDS reads may still be pending in
 // other waves (a barrier must precede any reuse of LDS).
-// Ad = AdapterArgs: the rows' adapters instead.
+// Ad = AdapterArgs: the rows' adapters instead, share of shares of them where
+// the tile mixes adapters.
 template <int B, typename Ad = NoAdapters>
 __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, int tn, int g0, int g1,
                                                  bool lowrank, f32x16 (&acc)[kBM / 32], uint8_t* lds,
-                                                 const Ad& ad = Ad{}) {
+                                                 const Ad& ad = Ad{}, int share = 0, int shares = 1) {
   constexpr int RB = kBM / 32;          // 8 row blocks of 32
   constexpr int LA = 4;                 // A-operand look-ahead, in MFMA steps
   constexpr int RING = 8;               // A-operand ring (64 steps per group = 8 laps)
@@ -281,7 +282,8 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
   const rsrc_t rs = make_rsrc(args.scales + (int64_t)nw0 * G, (uint32_t)n_valid * G * 4);
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    if (lowrank) adapter_mixed<32, 1>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc), lds, 512);
+    if (lowrank || shares > 1)
+      adapter_mixed<32, 1>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc), lds, 512, share, shares);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -940,7 +942,12 @@ __global__ __launch_bounds__(512, 1) void gemm_streamk_kernel(GemmArgs args, Str
     }
     f32x16 acc[kBM / 32];
     zero_acc(acc);
-    large_accumulate<B>(args, tm, tn, a, b, a == 0, acc, lds, ad...);
+    if constexpr (sizeof...(Ad) > 0) {
+      // split-K: the chunks share out the adapters of a tile that mixes them
+      large_accumulate<B>(args, tm, tn, a, b, a == 0, acc, lds, ad..., split_k ? w / tiles : 0, split_k ? sk.split : 1);
+    } else {
+      large_accumulate<B>(args, tm, tn, a, b, a == 0, acc, lds);
+    }
     __syncthreads();
     if (split_k) {
       // every chunk publishes its partial tile, then reduces and stores the
