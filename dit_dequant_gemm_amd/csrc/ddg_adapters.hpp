@@ -483,7 +483,7 @@ __device__ __forceinline__ void adapter_rows16(const AdapterArgs& ad, int m, int
 }
 
 // ---------------------------------------------------------------------------
-// T = s_a X D_a^T, as T^T = D_a X^T.  Workgroup (b, z; c; p): 16 RR rows, the
+// T = s_a X D_a^T, as T^T = D_a X^T.  Workgroup (b, z, c, p): 16 RR rows, the
 // row block's distinct adapters z, z + Z, ..., K chunk c (gpc groups of 128),
 // rank blocks of 16 from p RBLK on.  Its NW waves take runs of the chunk in
 // steps of 64 inputs and are summed through LDS in wave order.
@@ -507,7 +507,8 @@ struct AdapterDown {
   __bf16* t16;
   int m, k, r, count, chunks, gpc, parts;
   int z;                    // workgroups per row block
-  int run;                  // row blocks in a row before the next z
+  int rank_parts;           // workgroups along the rank
+  int run;                  // row blocks in a row before the next z; 0: all (z in blockIdx.z)
 };
 
 // Waves per workgroup: at most 8, and no more than leave room for a second
@@ -527,10 +528,15 @@ __global__ __launch_bounds__(64 * adapter_down_waves(RR, RBLK)) void adapter_dow
   const int lane = threadIdx.x & 63;
   const int lr = lane & 15, lq = lane >> 4;
   const int m = a.m, k = a.k, r = a.r;
-  const int runs = blockIdx.x / a.run, z = runs % a.z;
-  const int m0 = (runs / a.z * a.run + (blockIdx.x - runs * a.run)) * 16 * RR;
+  int block = blockIdx.x, z = blockIdx.z / a.rank_parts;
+  if (a.run > 0) {
+    const int runs = blockIdx.x / a.run;
+    z = runs % a.z;
+    block = runs / a.z * a.run + (blockIdx.x - runs * a.run);
+  }
+  const int m0 = block * 16 * RR;
   if (m0 >= m) return;
-  const int r0 = blockIdx.z * 16 * RBLK;
+  const int r0 = blockIdx.z % a.rank_parts * 16 * RBLK;
   const int kb = blockIdx.y * a.gpc * kGroup;               // chunk start (< k)
   const int kl = min(a.gpc * kGroup, k - kb);
   const int id[1] = {lane < 16 * RR ? adapter_of(a.rows, a.count, m0 + lane, m) : -1};

@@ -14,6 +14,9 @@
 //                         kernel that streams the packed weights once
 //   lowrank_t_kernel      T = bf16(X L1) for the low-rank branch (SVDQuant
 //                         article, section "技术原理详解")
+//   gemm_..._adapter_kernel, gemm_streamk_kernel<B, AdapterArgs>
+//                         the products with a low-rank adapter per row in
+//                         place of the one branch (ddg_adapters.hpp)
 #pragma once
 
 #include <type_traits>
