@@ -153,6 +153,9 @@ struct TileLanes {
   }
 };
 
+// Largest rank of adapter_tile.
+constexpr int kAdapterStraight = 32;
+
 template <int ROWS, int CB, typename Acc>
 __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n_total, int R, int m0, int col0,
                                              Acc (&acc)[256 / ROWS][CB]) {
@@ -163,7 +166,7 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n
 #pragma unroll
   for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + (threadIdx.x & 63), m);
   AdapterWalk<4> walk(id);
-  if (!walk.next(id) || walk.more()) return;
+  if (!walk.next(id) || walk.more() || R > kAdapterStraight) return;
   // T and U through buffer resources: one offset register instead of a 64-bit
   // address per row block; rows past M and columns past N read as zeros
   const uint32_t row_bytes = (uint32_t)R * 2;
@@ -215,29 +218,37 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n
     }
 }
 
-// A tile of several adapters, by the whole workgroup of n lanes.  T comes
-// through LDS, one rank step at a time (every adapter's turn reads it again),
-// and so does the list of the tile's adapters with their row masks, which the
-// first wave writes: with both at hand, U's loads of the next adapters are in
-// flight while one is multiplied, and row blocks without its rows are
-// skipped.  Of the list, entries share, share + shares, ... (workgroups that
-// split K share out the adapters too).  On return no wave needs the LDS.
-constexpr int kAdapterDepth = 4;                               // adapters whose U is in flight
-constexpr int kAdapterListAt = 3 * 256 * 64;                   // behind T's parts (32 ranks at most)
+// A tile of several adapters, or of one whose rank would make adapter_tile a
+// chain of load latencies, by the whole workgroup of n lanes.  T comes through
+// LDS, 64 ranks at a time (every adapter's turn reads it again), and so does
+// the list of the tile's adapters with their row masks, which the first wave
+// writes.  With both at hand the (adapter, rank step) pairs are one sequence:
+// U's loads of the next pairs are in flight while one is multiplied, and row
+// blocks without the adapter's rows are skipped.  Of the sequence, pairs
+// share, share + shares, ... (workgroups that split K share out the pairs
+// too).  On return no wave needs the LDS.
+constexpr int kAdapterDepth = 4;                               // pairs whose U is in flight
+constexpr int kAdapterFill = 64;                               // ranks of T in LDS
+constexpr int kAdapterListAt = kAdapterMaxParts * 256 * kAdapterFill * 2;
 constexpr int kAdapterEntry = 5;                               // 64-bit words: row masks, adapter
 
 template <int ROWS, int CB, typename Acc>
 __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int n_total, int R, int m0, int col0,
-                                              Acc (&acc)[256 / ROWS][CB], uint8_t* lds, int n, int share = 0,
+                                              Acc (&acc)[256 / ROWS][CB], uint8_t* lds, int share = 0,
                                               int shares = 1) {
   constexpr int RB = 256 / ROWS, KS = TileLanes<ROWS>::KS;
+  constexpr int N = ROWS == 32 ? 512 : 256;                    // lanes of the workgroup
+  constexpr int PIECES = KS / 8;                               // 16-byte pieces of a row's rank step
+  constexpr int PER = 256 * PIECES / N;                        // pieces per lane, step and part
+  constexpr int STEPS = kAdapterFill / KS;
   const TileLanes<ROWS> tl;
   const int tid = threadIdx.x;
   int id[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) id[j] = adapter_of(ad.rows, ad.count, m0 + 64 * j + (tid & 63), m);
   AdapterWalk<4> walk(id);
-  if (!walk.next(id) || !walk.more()) return;                  // the same in every wave
+  // the same in every wave
+  if (!walk.next(id) || (!walk.more() && R <= kAdapterStraight)) return;
   uint64_t* list = reinterpret_cast<uint64_t*>(lds + kAdapterListAt);
   if (tid < 64) {
     int count = 0;
@@ -253,42 +264,76 @@ __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int 
   }
   const uint32_t row_bytes = (uint32_t)R * 2;
   const uint32_t u_bytes = (uint32_t)max(0, min(CB * ROWS, n_total - col0)) * row_bytes;
-  for (int j0 = 0; j0 < R; j0 += KS) {
-    // T's parts of this rank step: [part][row][KS], zeros past the rank and past M
-    constexpr int PIECES = KS / 8;
-    for (int i = tid; i < ad.parts * 256 * PIECES; i += n) {
-      const int piece = i % PIECES, row = i / PIECES % 256, p = i / (PIECES * 256);
-      const int kk = j0 + 8 * piece;
-      const bf16x8 v = *reinterpret_cast<const bf16x8*>(ad.t16 + ((int64_t)p * m + min(m0 + row, m - 1)) * R +
-                                                        min(kk, R - 8));
-      *reinterpret_cast<bf16x8*>(lds + i * 16) = keep_or_zero(v, kk < R && m0 + row < m);
-    }
+  for (int f0 = 0; f0 < R; f0 += kAdapterFill) {
+    const int steps = (min(R - f0, kAdapterFill) + KS - 1) / KS;
+    // T of these ranks: [step][part][row][KS], zeros past the rank and past M
+    bf16x8 v[STEPS][kAdapterMaxParts][PER];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int p = 0; p < kAdapterMaxParts; ++p)
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int i = tid + e * N, kk = f0 + s * KS + 8 * (i % PIECES), row = m0 + i / PIECES;
+          if (s < steps && p < ad.parts)
+            v[s][p][e] = *reinterpret_cast<const bf16x8*>(ad.t16 + ((int64_t)p * m + min(row, m - 1)) * R + min(kk, R - 8));
+        }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int p = 0; p < kAdapterMaxParts; ++p)
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int i = tid + e * N, kk = f0 + s * KS + 8 * (i % PIECES), row = m0 + i / PIECES;
+          if (s < steps && p < ad.parts)
+            *reinterpret_cast<bf16x8*>(lds + ((s * ad.parts + p) * 256 * PIECES + i) * 16) =
+                keep_or_zero(v[s][p][e], kk < R && row < m);
+        }
     __syncthreads();
-    const int count = (__builtin_amdgcn_readfirstlane((int)list[0]) - share + shares - 1) / shares;     // this share's
-    const int kk = j0 + 8 * tl.q;
-    const uint32_t off = kk < R ? (uint32_t)tl.l * row_bytes + (uint32_t)kk * 2 : 0x80000000u;
+    const int count = __builtin_amdgcn_readfirstlane((int)list[0]);
+    // the pair (entry of the list, step) to load next and the one to multiply
+    int ahead = share / steps, ahead_s = share % steps, at = ahead, s = ahead_s;
+    auto advance = [&](int& entry, int& step) __attribute__((always_inline)) {
+      step += shares;
+      while (step >= steps) {
+        step -= steps;
+        ++entry;
+      }
+    };
     bf16x8 b[kAdapterDepth][CB];
-    auto load_u = [&](int i, bf16x8 (&u)[CB]) __attribute__((always_inline)) {
-      const int at = 1 + (share + min(i, count - 1) * shares) * kAdapterEntry;
-      const int adapter = __builtin_amdgcn_readfirstlane((int)list[at + 4]);
+    // what the list says of the pair to load next and of the one to multiply
+    // next, read a pair early; past the last entry: the last again, not used
+    uint32_t ahead_adapter, words[8];
+    auto read_ahead = [&]() __attribute__((always_inline)) {
+      ahead_adapter = (uint32_t)list[1 + min(ahead, count - 1) * kAdapterEntry + 4];
+    };
+    auto read_words = [&]() __attribute__((always_inline)) {
+      const uint32_t* from = reinterpret_cast<const uint32_t*>(list + 1 + min(at, count - 1) * kAdapterEntry);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) words[i] = from[i];
+    };
+    read_ahead();
+    read_words();
+    auto load_u = [&](bf16x8 (&u)[CB]) __attribute__((always_inline)) {
+      const int adapter = __builtin_amdgcn_readfirstlane((int)ahead_adapter);
       const rsrc_t ru = make_rsrc(ad.up + ((int64_t)adapter * n_total + col0) * R, u_bytes);
+      const int kk = f0 + ahead_s * KS + 8 * tl.q;
+      const uint32_t off = kk < R ? (uint32_t)tl.l * row_bytes + (uint32_t)kk * 2 : 0x80000000u;
 #pragma unroll
       for (int c = 0; c < CB; ++c)
         u[c] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(ru, off + c * ROWS * row_bytes, 0, 0));
+      advance(ahead, ahead_s);
+      read_ahead();
     };
-    if (count > 0) {
 #pragma unroll
-      for (int u = 0; u < kAdapterDepth; ++u) load_u(u, b[u]);
-    }
-    for (int i0 = 0; i0 < count; i0 += kAdapterDepth) {
+    for (int u = 0; u < kAdapterDepth; ++u) load_u(b[u]);
+    while (at < count) {
 #pragma unroll
       for (int u = 0; u < kAdapterDepth; ++u) {
-        if (i0 + u >= count) break;
+        if (at >= count) break;
         uint32_t bits[RB];
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
-          const uint32_t* words =
-              reinterpret_cast<const uint32_t*>(list + 1 + (share + (i0 + u) * shares) * kAdapterEntry);
           const uint32_t w = (uint32_t)__builtin_amdgcn_readfirstlane((int)words[rb * ROWS / 32]);
           bits[rb] = ROWS == 32 ? w : (w >> (rb * ROWS % 32)) & 0xFFFFu;
         }
@@ -302,17 +347,21 @@ __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int 
             for (int rb = 0; rb < RB; ++rb) acc[rb][c] = adapter_blow<ROWS>(broken, tl.mine(bits[rb]), acc[rb][c]);
           }
         }
+        const uint8_t* t_at = lds + s * ad.parts * 256 * PIECES * 16;
+        advance(at, s);
+        read_words();
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb) {
           if (bits[rb] == 0) continue;
           for (int p = 0; p < ad.parts; ++p) {
-            const bf16x8 t = *reinterpret_cast<const bf16x8*>(lds + ((p * 256 + rb * ROWS + tl.l) * PIECES + tl.q) * 16);
+            const bf16x8 t =
+                *reinterpret_cast<const bf16x8*>(t_at + ((p * 256 + rb * ROWS + tl.l) * PIECES + tl.q) * 16);
             const bf16x8 a = keep_or_zero(t, tl.mine(bits[rb]));
 #pragma unroll
             for (int c = 0; c < CB; ++c) acc[rb][c] = adapter_mfma(a, b[u][c], acc[rb][c]);
           }
         }
-        load_u(i0 + u + kAdapterDepth, b[u]);
+        load_u(b[u]);
       }
     }
     __syncthreads();                                           // T's LDS is free

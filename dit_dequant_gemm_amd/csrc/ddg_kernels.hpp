@@ -286,7 +286,7 @@ __device__ __forceinline__ void large_accumulate(const GemmArgs& args, int tm, i
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
     if (lowrank || shares > 1)
-      adapter_mixed<32, 1>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc), lds, 512, share, shares);
+      adapter_mixed<32, 1>(ad, args.m, args.n, args.r, m0, nw0 + wave * 32, tile_blocks(acc), lds, share, shares);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -585,7 +585,7 @@ __device__ __forceinline__ void n192_tile(const GemmArgs& args, int tm, int tn, 
     for (int c = 0; c < CB; ++c) acc[rb][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   if constexpr (std::is_same_v<Ad, AdapterArgs>) {
-    adapter_mixed<16, CB>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc, lds, 256);
+    adapter_mixed<16, CB>(ad, args.m, args.n, args.r, m0, nw0 + wave * 48, acc, lds);
     __builtin_amdgcn_sched_barrier(0);
   }
 

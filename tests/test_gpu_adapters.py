@@ -198,6 +198,27 @@ def test_a_broken_adapter_stays_with_its_rows(gpu_lib, m, n):
     assert torch.equal(got[others], base[others]) and bool(torch.isnan(got[1]).all())
 
 
+@pytest.mark.parametrize("m,n,k,a", [(300, 512, 2560, 1), (300, 512, 2560, 3), (300, 784, 256, 1), (700, 784, 384, 4)])
+def test_a_broken_high_rank_stays_with_its_rows(gpu_lib, m, n, k, a):
+    """One infinite entry of U past the first 64 ranks, in a tile of one
+    adapter (with rows of none) and in tiles that mix them, whole and split."""
+    _case(f"broken high rank {m}x{n}x{k} adapters={a}")
+    x, qw, pool = _setup(gpu_lib, m + n + a, m, n, k, 4, a, 128)
+    rows = _rows("each", m, a, 1)
+    rows[::5] = -1
+    for dt in (BF, F32):
+        want = gpu_lib.adapter_gemm(x, qw, pool, rows, out_dtype=dt)
+        keep = pool.up[0, 17, 100].clone()
+        pool.up[0, 17, 100] = float("inf")
+        got = gpu_lib.adapter_gemm(x, qw, pool, rows, out_dtype=dt)
+        pool.up[0, 17, 100] = keep
+        assert torch.equal(got[rows != 0], want[rows != 0])
+        hit = got[rows == 0]
+        assert not bool(torch.isfinite(hit[:, 17]).any())
+        hit[:, 17] = want[rows == 0][:, 17]
+        assert torch.equal(hit, want[rows == 0])
+
+
 def test_repeats_and_workspace(gpu_lib):
     """The same bits on every call, with a workspace of exactly the required
     bytes between guards, NaN inside; the output fully written."""
