@@ -104,7 +104,7 @@ struct RopeArgs {
   int ends[kRopeMaxAxes];
   int axes, pairs, dim, batch, tokens, w_f32;
   float eps, amplitude, signed_amplitude;    // signed: negative for the inverse
-  int lg, splits;           // set by the launcher
+  int lg, lt, splits;          // set by the launcher
 };
 // norm: DDG_NORM_*; half: the half layout
 hipError_t launch_rope(const RopeArgs& a, int norm, bool half, bool f32, int cus, hipStream_t stream);

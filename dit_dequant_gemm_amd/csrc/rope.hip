@@ -233,25 +233,33 @@ constexpr int kRopeWaves = 4;
 // head), handed to the lanes that need them through the wave's own LDS.
 struct WaveAngles {
   __attribute__((aligned(16))) float c[kRopeMaxHeadDim / 2], s[kRopeMaxHeadDim / 2];
-  __device__ __forceinline__ void compute(const RopeArgs& a, const int32_t* pos, int lane) {
+  __device__ __forceinline__ void fill(const RopeArgs& a, const int32_t* pos, int lane, int at) {
     for (int p = lane; p < a.pairs; p += 64) {
       float cp, sp;
       cos_sin_turns(pair_turns(a, pos, p), cp, sp);
-      c[p] = cp * a.amplitude;
-      s[p] = sp * a.signed_amplitude;
+      c[at + p] = cp * a.amplitude;
+      s[at + p] = sp * a.signed_amplitude;
     }
+  }
+  __device__ __forceinline__ void filled() const {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
+  __device__ __forceinline__ void compute(const RopeArgs& a, const int32_t* pos, int lane) {
+    fill(a, pos, lane, 0);
+    filled();
+  }
+  // at: the token's first pair
   template <int V, bool HALF>
-  __device__ __forceinline__ void take(const Slot<V, HALF>& k, int slot, float (&fc)[V], float (&fs)[V]) const {
+  __device__ __forceinline__ void take(const Slot<V, HALF>& k, int slot, float (&fc)[V], float (&fs)[V],
+                                       int at = 0) const {
     // runs of R consecutive pairs, aligned to R
     constexpr int R = HALF || V == 1 ? (V < 4 ? V : 4) : V / 2;
     typedef float run __attribute__((ext_vector_type(R)));
 #pragma unroll
     for (int j = 0; j < V; j += R) {
-      const int p = k.pair(slot, j);
+      const int p = at + k.pair(slot, j);
       const run rc = *reinterpret_cast<const run*>(c + p), rs = *reinterpret_cast<const run*>(s + p);
 #pragma unroll
       for (int e = 0; e < R; ++e) {
@@ -267,24 +275,54 @@ struct WaveAngles {
 // slot per lane, 64 >> lg heads at a time, query heads first.  V = 1 gives a
 // head to the whole wave, up to NS slots per lane.  The next heads' values
 // are loaded before the current ones are turned, the first ones before the
-// angles are computed.
-template <typename T, int V, bool HALF, bool NORM>
+// angles are computed.  The norm weights go through LDS once per workgroup:
+// loaded by every lane where it needs them, q's and k's were four latencies
+// in a row.  Where q and k have few heads, PACK gives a wave's lanes to several
+// tokens, as many as keep the heads' lanes busy and their angles in LDS: a
+// vector instruction costs the same for 8 lanes as for 64, and with 1 + 1
+// heads those outweigh the bytes.
+template <typename T, int V, bool HALF, bool NORM, bool PACK>
 __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) {
   constexpr int NS = V == 1 ? kRopeMaxHeadDim / 128 : 1;
   __shared__ WaveAngles ang[kRopeWaves];
+  __shared__ __attribute__((aligned(16))) float weights[NORM ? 2 * kRopeMaxHeadDim : 1];     // q's, k's
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int sl = lane & ((1 << a.lg) - 1), hl = lane >> a.lg, hpw = 64 >> a.lg;
+  // PACK: hpw heads of each of 1 << lt tokens at a time
+  const int lt = PACK ? a.lt : 0, hpw = 64 >> (a.lg + lt);
+  const int sl = lane & ((1 << a.lg) - 1), hl = (lane >> a.lg) & (hpw - 1), tk = PACK ? lane / (hpw << a.lg) : 0;
   const int slots = a.dim / (2 * V);
+  constexpr int WL = 2 * kRopeMaxHeadDim / (64 * kRopeWaves);                               // per lane
+  float w_mine[WL];
+  if constexpr (NORM) {
+#pragma unroll
+    for (int i = 0; i < WL; ++i) {
+      const int at = threadIdx.x + i * 64 * kRopeWaves, e = min(at % kRopeMaxHeadDim, a.dim - 1);
+      load_weight<1>(at < kRopeMaxHeadDim ? a.q : a.k, a.w_f32, e, reinterpret_cast<float(&)[1]>(w_mine[i]));
+    }
+  }
+  bool weights_there = !NORM;
   const int gq = (a.q.heads + hpw - 1) / hpw, gk = (a.k.heads + hpw - 1) / hpw, groups = gq + gk;
-  const int64_t total = (int64_t)a.batch * a.tokens * a.splits;
+  const int rows = a.batch * a.tokens;
+  const int64_t total = PACK ? ((int64_t)rows + (1 << lt) - 1) >> lt : (int64_t)rows * a.splits;
   const float inv_dim = 1.0f / (float)a.dim;
-  for (int64_t w = (int64_t)blockIdx.x * kRopeWaves + wave; w < total; w += (int64_t)gridDim.x * kRopeWaves) {
-    const int row = (int)(w / a.splits), part = (int)(w - (int64_t)row * a.splits);
-    const int b = row / a.tokens, t = row - b * a.tokens;
-    const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
-    const int g0 = (int)((int64_t)part * groups / a.splits), g1 = (int)((int64_t)(part + 1) * groups / a.splits);
-
+  for (int64_t w0 = (int64_t)blockIdx.x * kRopeWaves; w0 < total; w0 += (int64_t)gridDim.x * kRopeWaves) {
+    // past the last wave's work: its work again, not stored (every wave
+    // reaches the barrier)
+    bool live = w0 + wave < total;
+    const int64_t w = live ? w0 + wave : total - 1;
+    int row = (int)w, part = 0, g0 = 0, g1 = groups;
+    if constexpr (PACK) {
+      const int64_t mine = (w << lt) + tk;
+      live = live && mine < rows;
+      row = (int)min(mine, (int64_t)rows - 1);
+    } else if (a.splits > 1) {                         // total < 2^31
+      row = (int)w / a.splits;
+      part = (int)w - row * a.splits;
+      g0 = part * groups / a.splits;
+      g1 = (part + 1) * groups / a.splits;
+    }
+    const int b = a.batch > 1 ? row / a.tokens : 0, t = row - b * a.tokens;
     Chunk<T, V> next[NS][2];
     auto load_group = [&](int g) {
       const bool is_q = g < gq;
@@ -301,13 +339,28 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
     };
     load_group(g0);
 
-    ang[wave].compute(a, pos, lane);
+    if constexpr (PACK) {
+      for (int i = 0; i < 1 << lt; ++i) {
+        const int at = (int)min((w << lt) + i, (int64_t)rows - 1);
+        const int bi = a.batch > 1 ? at / a.tokens : 0;
+        ang[wave].fill(a, a.pos + (int64_t)bi * a.pos_batch + (int64_t)(at - bi * a.tokens) * a.axes, lane, i * a.pairs);
+      }
+      ang[wave].filled();
+    } else {
+      ang[wave].compute(a, a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes, lane);
+    }
     float c[NS][V], s[NS][V];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
       const int slot = sl + 64 * i;
       const Slot<V, HALF> k(a, slot);
-      if (slot < slots && k.turns) ang[wave].template take<V, HALF>(k, slot, c[i], s[i]);
+      if (slot < slots && k.turns) ang[wave].template take<V, HALF>(k, slot, c[i], s[i], tk * a.pairs);
+    }
+    if (!weights_there) {
+#pragma unroll
+      for (int i = 0; i < WL; ++i) weights[threadIdx.x + i * 64 * kRopeWaves] = w_mine[i];
+      lds_barrier();
+      weights_there = true;
     }
 
 #pragma unroll
@@ -321,8 +374,11 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
           const Slot<V, HALF> k(a, min(sl + 64 * i, slots - 1));
-          load_weight<V>(x, a.w_f32, k.ia, wa[i]);
-          load_weight<V>(x, a.w_f32, k.ib, wb[i]);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            wa[i][j] = weights[z * kRopeMaxHeadDim + k.ia + j];
+            wb[i][j] = weights[z * kRopeMaxHeadDim + k.ib + j];
+          }
         }
       }
       for (int g = lo; g < hi; ++g) {
@@ -358,7 +414,7 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
         for (int i = 0; i < NS; ++i) {
           const int slot = sl + 64 * i;
           const Slot<V, HALF> k(a, slot);
-          if (slot >= slots || h >= x.heads) continue;
+          if (!live || slot >= slots || h >= x.heads) continue;
           if (k.turns) turn_slot<V, HALF>(fa[i], fb[i], c[i], s[i]);
           store_vals<T, V>(x.y, base + k.ia, fa[i]);
           store_vals<T, V>(x.y, base + k.ib, fb[i]);
@@ -382,9 +438,9 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_token_wave_kernel(RopeAr
   const int tensors = a.k.heads > 0 ? 2 : 1;
   const int64_t total = (int64_t)a.batch * a.tokens * tensors;
   for (int64_t w = (int64_t)blockIdx.x * kRopeWaves + wave; w < total; w += (int64_t)gridDim.x * kRopeWaves) {
-    const int row = (int)(w / tensors);
-    const RopeTensor& x = w - (int64_t)row * tensors ? a.k : a.q;
-    const int b = row / a.tokens, t = row - b * a.tokens;
+    const int row = (int)(tensors > 1 ? w >> 1 : w);
+    const RopeTensor& x = tensors > 1 && (w & 1) ? a.k : a.q;
+    const int b = a.batch > 1 ? row / a.tokens : 0, t = row - b * a.tokens;
     const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
     const Slot<V, HALF> k(a, min(sl, slots - 1));
     Chunk<T, V> raw[G][2];
@@ -450,7 +506,7 @@ __global__ __launch_bounds__(64 * kRopeMaxWaves) void rope_token_kernel(RopeArgs
   const int slots = a.dim / (2 * V), items = x.heads * slots;
   const int64_t rows = (int64_t)a.batch * a.tokens;
   auto at = [&](bool out, int64_t row, int h) -> int64_t {
-    const int b = (int)(row / a.tokens), t = (int)(row - (int64_t)b * a.tokens);
+    const int b = a.batch > 1 ? (int)row / a.tokens : 0, t = (int)row - b * a.tokens;
     return out ? (int64_t)b * x.yb + (int64_t)t * x.yt + (int64_t)h * x.yh
                : (int64_t)b * x.xb + (int64_t)t * x.xt + (int64_t)h * x.xh;
   };
@@ -486,7 +542,7 @@ __global__ __launch_bounds__(64 * kRopeMaxWaves) void rope_token_kernel(RopeArgs
   int buf = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
     if (a.pairs > 0) {
-      const int b = (int)(row / a.tokens), t = (int)(row - (int64_t)b * a.tokens);
+      const int b = a.batch > 1 ? (int)row / a.tokens : 0, t = (int)row - b * a.tokens;
       const int32_t* pos = a.pos + (int64_t)b * a.pos_batch + (int64_t)t * a.axes;
       for (int p = tid; p < a.pairs; p += n) {
         float c, s;
@@ -601,13 +657,27 @@ hipError_t launch_v(RopeArgs a, int norm, int cus, hipStream_t stream) {
   // a token's heads go to several waves while tokens alone leave waves idle
   const int64_t want = (int64_t)cus * 16;
   a.splits = (int)std::max<int64_t>(1, std::min<int64_t>(groups, want / rows));
-  const int64_t waves = rows * a.splits;
+  int64_t waves = rows * a.splits;
+  a.lt = 0;
+  if (V > 1) {
+    const int most_heads = std::max(a.q.heads, a.k.heads);
+    while (most_heads <= hpw >> (a.lt + 1) && a.pairs << (a.lt + 1) <= kRopeMaxHeadDim / 2 &&
+           rows >> (a.lt + 1) >= (int64_t)cus * 8)
+      ++a.lt;
+    if (a.lt > 0) waves = (rows + (1 << a.lt) - 1) >> a.lt;
+  }
   const int64_t grid = std::min<int64_t>((waves + kRopeWaves - 1) / kRopeWaves, (int64_t)cus * 64);
-  if (norm == DDG_NORM_HEAD)
-    rope_head_kernel<T, V, HALF, true><<<dim3((unsigned)grid), dim3(64 * kRopeWaves), 0, stream>>>(a);
-  else
-    rope_head_kernel<T, V, HALF, false><<<dim3((unsigned)grid), dim3(64 * kRopeWaves), 0, stream>>>(a);
-  return hipGetLastError();
+  auto launch = [&](auto kernel) {
+    kernel<<<dim3((unsigned)grid), dim3(64 * kRopeWaves), 0, stream>>>(a);
+    return hipGetLastError();
+  };
+  if constexpr (V > 1) {
+    if (a.lt > 0)
+      return norm == DDG_NORM_HEAD ? launch(rope_head_kernel<T, V, HALF, true, true>)
+                                   : launch(rope_head_kernel<T, V, HALF, false, true>);
+  }
+  return norm == DDG_NORM_HEAD ? launch(rope_head_kernel<T, V, HALF, true, false>)
+                               : launch(rope_head_kernel<T, V, HALF, false, false>);
 }
 
 template <typename T, int V>

@@ -164,6 +164,46 @@ def test_many_heads(gpu_lib, norm, hq, hk, dim):
         _check(got, ref, mag * (2 if hq * dim > 16384 else 1), (hq, dim, norm))
 
 
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("hq,hk,dim,rot", [(1, 1, 128, 128), (3, 1, 64, 32), (2, 2, 72, 72), (4, 2, 128, 64), (1, 1, 16, 0),
+                                           (1, 2, 40, 40), (5, 3, 96, 48), (2, 1, 256, 256)])
+def test_few_heads_of_many_tokens(gpu_lib, dtype, layout, hq, hk, dim, rot):
+    """Waves that take several tokens: the formulas, the bits of a call over
+    few tokens, a position row per batch entry, in place, and the rows behind."""
+    b, s = 3, 3461 if hq > 2 else 12289
+    _case(f"few heads {dtype} {layout} {hq}+{hk} heads of {dim}, {rot} rotated, {b}x{s}")
+    rng = np.random.default_rng(dim + rot + hq)
+    pos = rng.integers(0, 5000, (b, s, 1)).astype(np.int32)
+    f = _freqs(rot // 2)
+    post, ft = torch.from_numpy(pos).cuda(), torch.from_numpy(f).cuda()
+    buf = torch.full((b * s + 9, (hq + hk) * dim + 8), float("nan"), dtype=dtype, device="cuda")
+    vals = torch.from_numpy(rng.standard_normal((b * s, (hq + hk) * dim)).astype(np.float32)).to(dtype)
+    buf[:b * s, :(hq + hk) * dim] = vals.cuda()
+    rows = buf[:b * s].view(b, s, -1)
+    q = rows[..., :hq * dim].view(b, s, hq, dim)
+    k = rows[..., hq * dim:(hq + hk) * dim].view(b, s, hk, dim)
+    vals = vals.double().numpy().reshape(b, s, -1)
+    wq, wk = (torch.from_numpy(rng.uniform(0.5, 1.5, dim).astype(np.float32)).to(dtype).cuda() for _ in range(2))
+    yq, yk = gpu_lib.qk_norm_rope(q, k, post, ft, q_weight=wq, k_weight=wk, norm="head", layout=layout)
+    for y, v, w, what in ((yq, vals[..., :hq * dim].reshape(b, s, hq, dim), wq, "q"),
+                          (yk, vals[..., hq * dim:].reshape(b, s, hk, dim), wk, "k")):
+        ref, mag = _reference(v, pos, f, (rot // 2,), layout, weight=w.double().cpu().numpy(), norm="head")
+        _check(y, ref, mag, what)
+    lo = s - 29                                           # a call over few tokens: the same bits
+    fq, fk = gpu_lib.qk_norm_rope(q[:, lo:], k[:, lo:], post[:, lo:].contiguous(), ft, q_weight=wq, k_weight=wk,
+                                  norm="head", layout=layout)
+    assert torch.equal(fq, yq[:, lo:]) and torch.equal(fk, yk[:, lo:])
+    if rot:
+        turned = gpu_lib.rope(q, post, ft, layout=layout)
+        assert torch.equal(turned[:, lo:], gpu_lib.rope(q[:, lo:], post[:, lo:].contiguous(), ft,
+                                                            layout=layout))
+    gpu_lib.qk_norm_rope(q, k, post, ft, q_weight=wq, k_weight=wk, norm="head", layout=layout, out_q=q,
+                         out_k=k)
+    assert torch.equal(q, yq) and torch.equal(k, yk)
+    assert bool(torch.isnan(buf[b * s:]).all()) and bool(torch.isnan(buf[:, (hq + hk) * dim:]).all())
+
+
 def test_far_positions(gpu_lib):
     """The angle stays exact where float32 has lost it, up to the largest int32."""
     _case("far positions")
