@@ -738,7 +738,21 @@ class AdapterPool:
             raise ValueError("down and up disagree in their adapters or rank")
         if down.device != up.device or down.device != scales.device:
             raise ValueError("down, up and scales must be on one device")
-        self.down, self.up, self.scales = down, up, scales
+        self._down, self._up, self._scales = down, up, scales
+
+    # what was checked together stays together: the values may change, the
+    # tensors may not
+    @property
+    def down(self) -> torch.Tensor:
+        return self._down
+
+    @property
+    def up(self) -> torch.Tensor:
+        return self._up
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._scales
 
     @classmethod
     def stack(cls, adapters, qw: QWeight) -> "AdapterPool":
@@ -779,7 +793,7 @@ def adapter_gemm(x: torch.Tensor, qw: QWeight, pool: AdapterPool, rows: torch.Te
     capture K is not split (see dequant_gemm)."""
     x = _prep_x(x, qw)
     m, k, n, dev = x.shape[0], qw.k, qw.n, x.get_device()
-    down, up = pool.down, pool.up
+    down, up = pool._down, pool._up
     adapters, r, pk = down.shape
     if rows.dtype != torch.int32 or rows.shape != (m,) or not rows.is_contiguous():
         raise ValueError("rows must be dense int32, one entry per row of x")
@@ -802,7 +816,7 @@ def adapter_gemm(x: torch.Tensor, qw: QWeight, pool: AdapterPool, rows: torch.Te
                 wbytes = min(wbytes, adapter_workspace_bytes(m, n, k, r, False))
         _check(load_library().ddg_adapter_gemm(
             x.data_ptr(), m, k, qw.packed.data_ptr(), qw.scales.data_ptr(), qw.bits, n, down.data_ptr(),
-            up.data_ptr(), pool.scales.data_ptr(), adapters, r, rows.data_ptr(), y.data_ptr(),
+            up.data_ptr(), pool._scales.data_ptr(), adapters, r, rows.data_ptr(), y.data_ptr(),
             DDG_F32 if y.dtype == torch.float32 else DDG_BF16, workspace.data_ptr(), wbytes,
             _stream_ptr(x.device)), "ddg_adapter_gemm")
     return y

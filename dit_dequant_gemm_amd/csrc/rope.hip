@@ -73,8 +73,8 @@ struct Chunk {
       const u32x2 t = *reinterpret_cast<const u32x2*>(p);
       w[0] = t[0];
       w[1] = t[1];
-    } else if constexpr (sizeof(T) == 4) {
-      w[0] = __builtin_bit_cast(uint32_t, (float)*p);
+    } else if constexpr (sizeof(T) * V == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
@@ -111,6 +111,10 @@ __device__ __forceinline__ void store_vals(void* base, int64_t i, const float (&
                                          pack_bf16x2(f[6], f[7])};
   } else if constexpr (sizeof(T) == 2 && V == 4) {
     *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+  } else if constexpr (sizeof(T) == 4 && V == 2) {
+    *reinterpret_cast<f32x2*>(p) = f32x2{f[0], f[1]};
+  } else if constexpr (sizeof(T) == 2 && V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(f[0], f[1]);
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) p[j] = (T)f[j];
@@ -699,13 +703,18 @@ bool chunks_of(const RopeArgs& a, int es, int v) {
 }  // namespace
 
 hipError_t launch_rope(const RopeArgs& a, int norm, bool half, bool f32, int cus, hipStream_t stream) {
-  // the widest chunks that the head, the rotated part and the rows allow
+  // the widest chunks that the head, the rotated part and the rows allow; two
+  // values (an even number of pairs, as 36 rotated values of 72) while a head's
+  // slots are the lanes of a wave at most
+  const bool two = a.dim <= 256;
   if (f32) {
     if (chunks_of(a, 4, 4)) return launch_layout<float, 4>(a, norm, half, cus, stream);
+    if (two && chunks_of(a, 4, 2)) return launch_layout<float, 2>(a, norm, half, cus, stream);
     return launch_layout<float, 1>(a, norm, half, cus, stream);
   }
   if (chunks_of(a, 2, 8)) return launch_layout<__bf16, 8>(a, norm, half, cus, stream);
   if (chunks_of(a, 2, 4)) return launch_layout<__bf16, 4>(a, norm, half, cus, stream);
+  if (two && chunks_of(a, 2, 2)) return launch_layout<__bf16, 2>(a, norm, half, cus, stream);
   return launch_layout<__bf16, 1>(a, norm, half, cus, stream);
 }
 

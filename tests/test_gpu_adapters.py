@@ -272,6 +272,22 @@ def test_padded_inputs_and_stack(gpu_lib):
     assert float((y.double() - want).norm() / want.norm()) < 1e-5
 
 
+def test_a_pool_keeps_its_tensors(gpu_lib):
+    """Tensors that were checked together cannot be exchanged one by one; their
+    values may change between calls."""
+    _case("pool tensors")
+    x, qw, pool = _setup(gpu_lib, 2, 8, 64, 256, 4, 2, 16)
+    for name in ("down", "up", "scales"):
+        with pytest.raises(AttributeError):
+            setattr(pool, name, getattr(pool, name)[:1])
+    rows = _rows("each", 8, 2, 0)
+    first = gpu_lib.adapter_gemm(x, qw, pool, rows, out_dtype=F32)
+    pool.scales.mul_(2.0)
+    again = gpu_lib.adapter_gemm(x, qw, pool, rows, out_dtype=F32)
+    assert not torch.equal(first, again)
+    _check(again, _reference(gpu_lib, x, qw, pool, rows), 256, 16, "changed scales")
+
+
 def test_refused_calls(gpu_lib):
     _case("refusals")
     x, qw, pool = _setup(gpu_lib, 1, 8, 64, 256, 4, 2, 16)

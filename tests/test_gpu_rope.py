@@ -167,7 +167,7 @@ def test_many_heads(gpu_lib, norm, hq, hk, dim):
 @pytest.mark.parametrize("layout", ["interleaved", "half"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("hq,hk,dim,rot", [(1, 1, 128, 128), (3, 1, 64, 32), (2, 2, 72, 72), (4, 2, 128, 64), (1, 1, 16, 0),
-                                           (1, 2, 40, 40), (5, 3, 96, 48), (2, 1, 256, 256)])
+                                           (1, 2, 40, 40), (5, 3, 96, 48), (2, 1, 256, 256), (2, 1, 72, 36), (4, 4, 76, 20)])
 def test_few_heads_of_many_tokens(gpu_lib, dtype, layout, hq, hk, dim, rot):
     """Waves that take several tokens: the formulas, the bits of a call over
     few tokens, a position row per batch entry, in place, and the rows behind."""
