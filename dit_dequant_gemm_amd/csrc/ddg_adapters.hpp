@@ -131,9 +131,11 @@ struct AdapterWalk {
 // group's loads, where its latencies overlap theirs.  A tile that mixes
 // adapters (adapter_mixed) is done ahead of those loads, while the LDS is
 // free: a loop over adapters behind them made the compiler spill around the K
-// loop and cost every tile 10 us, also without any adapter (32760 x 15360 x
-// 5120: 4018 us for the product alone, 4311 with rows that name none; now 4150
-// and 4175).
+// loop and cost every tile 10 us, also without any adapter.  The branch's
+// matrix work is 1 to 2% of the product's; with its latencies and the pre-pass
+// it costs 4% at 4096 x 13824 x 5120 and rank 16 (550 us alone, 571 with one
+// adapter or requests in runs) and 6% at 32760 x 15360 x 5120 and rank 32 (4.04
+// and 4.28 ms, 1.2 PFLOP/s).
 //
 // ROWS x (256 / ROWS) row blocks, CB column blocks of ROWS from column col0
 // on; lane (row or column l, k part q) of the operands.
@@ -219,14 +221,17 @@ __device__ __forceinline__ void adapter_tile(const AdapterArgs& ad, int m, int n
 }
 
 // A tile of several adapters, or of one whose rank would make adapter_tile a
-// chain of load latencies, by the whole workgroup of n lanes.  T comes through
+// chain of load latencies (1517 x 496 x 2560, rank 128: 94 us there, 64 here),
+// by the whole workgroup.  T comes through
 // LDS, 64 ranks at a time (every adapter's turn reads it again), and so does
 // the list of the tile's adapters with their row masks, which the first wave
 // writes.  With both at hand the (adapter, rank step) pairs are one sequence:
 // U's loads of the next pairs are in flight while one is multiplied, and row
 // blocks without the adapter's rows are skipped.  Of the sequence, pairs
 // share, share + shares, ... (workgroups that split K share out the pairs
-// too).  On return no wave needs the LDS.
+// too).  On return no wave needs the LDS.  A pair over a whole tile takes 1.3
+// us, half of it matrix instructions (4096 x 5120 x 5120, 256 adapters in
+// every tile: 880 us, 241 with one).
 constexpr int kAdapterDepth = 4;                               // pairs whose U is in flight
 constexpr int kAdapterFill = 64;                               // ranks of T in LDS
 constexpr int kAdapterListAt = kAdapterMaxParts * 256 * kAdapterFill * 2;
@@ -372,7 +377,9 @@ __device__ __forceinline__ void adapter_mixed(const AdapterArgs& ad, int m, int 
 // At most 64 rows.  The workgroup adds T's chunks up into LDS once
 // (AdapterStage) as bf16 parts; its K-split waves share out the distinct
 // adapters, and the first two adapters' U of each wave are loaded before the
-// K loop (adapter_first) and used behind it.
+// K loop (adapter_first) and used behind it.  Bound by latencies: 16 x 15360 x
+// 5120 with 16 adapters of rank 16 takes 25.5 us where the product alone takes
+// 18.8, 37 x 5120 x 13824 at rank 64 60 us and 50.
 // ---------------------------------------------------------------------------
 constexpr size_t adapter_stage_bytes(int rows) { return (size_t)kAdapterMaxParts * rows * 128 * 2; }
 
@@ -543,7 +550,8 @@ __device__ __forceinline__ void adapter_rows16(const AdapterArgs& ad, int m, int
 // the line accesses bound the kernel: 32760 x 5120 at rank 32 took 128 us, with
 // the rows read once more 222.)  Row r's 16-byte piece c sits in slot
 // c ^ (r & 7), so that the operand reads spread over the banks.
-// Rows without an adapter are not written (no product reads them).
+// Rows without an adapter are not written (no product reads them).  32760 x
+// 5120 at rank 32: 92 to 97 us (335 MB, 3.5 TB/s); 4096 rows at rank 16: 11.4.
 //   PARTS: one chunk; T's bf16 parts to t16 (parts x m x r)
 //   else:  the chunk's float32 sums to part (chunks x m x r)
 // ---------------------------------------------------------------------------

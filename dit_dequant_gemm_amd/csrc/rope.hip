@@ -10,7 +10,10 @@
 // rounding at the store is float32; the angle is float64 (a position of 10^6
 // times a frequency near 1 leaves float32 no fraction of a turn to speak of).
 //
-// Bound by HBM: each value is read and written once.  The sines and cosines
+// Bound by HBM: each value is read and written once (bf16: norm per head and
+// rotation of 32760 tokens of 40 + 40 heads of 128 266 us, 5.0 TB/s; rotation
+// alone of 32768 tokens of 24 heads 83 us, 4.8 TB/s; a large copy reaches 5.3
+// to 5.6), with few tokens by the launch (one token 3.8 us).  The sines and cosines
 // belong to a (token, pair) and not to a head, so a wave computes those of its
 // lanes' pairs once per token and keeps them in registers over the heads; no
 // table is read.
@@ -284,7 +287,8 @@ struct WaveAngles {
 // in a row.  Where q and k have few heads, PACK gives a wave's lanes to several
 // tokens, as many as keep the heads' lanes busy and their angles in LDS: a
 // vector instruction costs the same for 8 lanes as for 64, and with 1 + 1
-// heads those outweigh the bytes.
+// heads those outweigh the bytes (33610 tokens of 1 + 1 heads of 128: 41 us
+// without, 20 with).
 template <typename T, int V, bool HALF, bool NORM, bool PACK>
 __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) {
   constexpr int NS = V == 1 ? kRopeMaxHeadDim / 128 : 1;
@@ -431,7 +435,8 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_head_kernel(RopeArgs a) 
 // The norm over all heads of a token where one wave can hold q (or k) of a
 // token: job 2 row + z is tensor z of token row, its lanes as in the head
 // kernel, G groups of heads in registers between the sum of squares and the
-// rotation.  No barrier, and every wave's loads are all in flight at once.
+// rotation.  No barrier, and every wave's loads are all in flight at once (2 x
+// 4099 tokens of 40 + 40 heads of 128, bf16: 69 us, 4.9 TB/s).
 template <typename T, int V, bool HALF, int G>
 __global__ __launch_bounds__(64 * kRopeWaves) void rope_token_wave_kernel(RopeArgs a) {
   __shared__ WaveAngles ang[kRopeWaves];
@@ -499,7 +504,8 @@ __global__ __launch_bounds__(64 * kRopeWaves) void rope_token_wave_kernel(RopeAr
 // token's cosines and sines are computed once into LDS.  The weights of a
 // lane's items stay in registers over the tokens, and the next token's values
 // are loaded before the current one is finished.  Items past a lane's NH (more
-// than 1024 slots) are read twice, the second time from the L2.
+// than 1024 slots) are read twice, the second time from the L2.  4096 tokens of
+// 96 + 96 heads of 128, bf16: 100 us, 4.0 TB/s (a barrier per token).
 constexpr int kRopeMaxWaves = 8;
 template <typename T, int V, bool HALF, int NH>
 __global__ __launch_bounds__(64 * kRopeMaxWaves) void rope_token_kernel(RopeArgs a) {
@@ -705,7 +711,8 @@ bool chunks_of(const RopeArgs& a, int es, int v) {
 hipError_t launch_rope(const RopeArgs& a, int norm, bool half, bool f32, int cus, hipStream_t stream) {
   // the widest chunks that the head, the rotated part and the rows allow; two
   // values (an even number of pairs, as 36 rotated values of 72) while a head's
-  // slots are the lanes of a wave at most
+  // slots are the lanes of a wave at most (8192 tokens of 16 + 16 such heads 32
+  // us, 83 with a wave per head)
   const bool two = a.dim <= 256;
   if (f32) {
     if (chunks_of(a, 4, 4)) return launch_layout<float, 4>(a, norm, half, cus, stream);
